@@ -133,7 +133,8 @@ VX_API uint64_t vx_launch_count(void);
 /* Clears the status word at the start of ws (async on stream). */
 VX_API vx_status vx_status_reset(void *ws, cudaStream_t stream);
 /* Synchronises `stream`, then returns VX_ERR_DEVICE_TIMEOUT if a kernel
- * recorded an expired wait in ws, else VX_OK (or VX_ERR_CUDA). */
+ * recorded an expired wait in ws, VX_ERR_INVALID_ARG if a paged-cache call
+ * recorded a bad page or length there, else VX_OK (or VX_ERR_CUDA). */
 VX_API vx_status vx_status_check(const void *ws, cudaStream_t stream);
 
 /* Fills the packed layout of one layer.  packed_wqkv: [3*HD, d] bf16,
@@ -333,6 +334,162 @@ VX_API vx_status vx_stream_step(const vx_layer_cfg *cfg, const vx_layer_weights 
                          const vx_kv_ring *ring, const float *x_new, float *y, int n_new,
                          const void *final_g, void *ws, size_t ws_bytes, cudaStream_t stream);
 VX_API size_t vx_stream_step_workspace(const vx_layer_cfg *cfg, int S, int n_new);
+
+/* ------------------------------------------------------------ paged cache */
+
+/* A K/V cache of pages, for sequences of any length, grouped heads and
+ * batches of unequal sequences (the ring above holds a fixed window of one
+ * length per stream; the Core AI card's streaming encoder keeps an
+ * append-only frame buffer without eviction, section "Usage / Known
+ * limitations").
+ *
+ * Layer l, page p, K/V head h, row r of k and v: [n_layers][n_pages]
+ * [n_kv_heads][page_size][head_dim] of dtype dt.  Slot j of sequence s is row
+ * j % page_size of page table[s * max_pages + j / page_size]; every layer uses
+ * the same table.  lens[s] counts the tokens that sequence s holds (slots
+ * 0 .. lens[s] - 1); pos[s] counts the tokens ever appended to it, the
+ * position of its next token: the two part once tokens are evicted.  acc (may
+ * be NULL) is the accumulated attention weight of each slot,
+ * [n_layers][n_pages][n_kv_heads][page_size] fp32.
+ * All pointers are device pointers of the caller, who hands out the pages
+ * (table entries of slots that no call touches may hold anything, -1 say).
+ * head_dim 64 or 128, page_size 1 .. 65536, max_pages * page_size < 2^30.
+ *
+ * A call processes a chunk of new tokens: sequence s owns the rows
+ * q_start[s] .. q_start[s + 1] - 1 of the token tensors (device int32
+ * [n_seqs + 1], rising; a sequence may have none).  n_tokens is the number of
+ * rows of those tensors, max_q a bound on the rows of one sequence (rows past
+ * it are not processed).  Rows before q_start[0] and from q_start[n_seqs] on
+ * are left as they were.  For each layer vx_paged_append, then
+ * vx_paged_attn_fwd; after the last layer vx_paged_advance once.
+ *
+ * What a kernel finds wrong on the device it records in the status word
+ * (vx_status_check then returns VX_ERR_INVALID_ARG): a page outside 0 ..
+ * n_pages - 1 reads as zeros and is not written, tokens past the table's
+ * max_pages * page_size slots are neither stored nor attended. */
+typedef struct vx_paged_cache {
+  void *k;
+  void *v;
+  float *acc;
+  const int32_t *table;
+  int64_t *lens;
+  int64_t *pos;
+  vx_dtype dt;
+  int n_layers, n_pages, page_size, n_kv_heads, head_dim, n_seqs, max_pages;
+} vx_paged_cache;
+
+/* Rows of heads inside a larger tensor: head h of row t starts at element
+ * t * row + h * head of p, its head_dim elements contiguous. */
+typedef struct vx_rows {
+  void *p;
+  int64_t row, head;
+} vx_rows;
+
+typedef enum vx_rope_scaling {
+  VX_ROPE_NONE = 0,
+  VX_ROPE_LINEAR = 1,  /* f_m / factor                                           */
+  VX_ROPE_NTK = 2,     /* theta * factor^(rot_dim / (rot_dim - 2)) for theta     */
+  VX_ROPE_YARN = 3     /* g f_m + (1 - g) f_m / factor with
+                          g = clamp((orig_len f_m / 2 pi - beta_slow) / (beta_fast - beta_slow), 0, 1),
+                          cosine and sine times mscale                           */
+} vx_rope_scaling;
+
+/* Rotary positions: the first rot_dim elements of a head (even, <= head_dim;
+ * 0 = head_dim) are rotated in pairs (m, m + rot_dim / 2), or (2m, 2m + 1)
+ * when interleaved, by position * f_m, f_m = theta^(-2m / rot_dim); the others
+ * are copied.  scaling != VX_ROPE_NONE needs factor >= 1.  VX_ROPE_YARN needs
+ * orig_len >= 1 and beta_fast > beta_slow; mscale 0 selects
+ * 0.1 ln(factor) + 1.  The angle is kept as a 64-bit fraction of a turn, so
+ * positions of any size are exact to better than 2^-24 of a radian. */
+typedef struct vx_rope_cfg {
+  int rot_dim;
+  int interleaved;
+  int scaling;
+  int orig_len;
+  double theta;
+  double factor;
+  double beta_fast, beta_slow;
+  double mscale;
+} vx_rope_cfg;
+
+/* y = rotary(x) at positions pos[t] (device int64 [n_tokens], any sign), for
+ * n_heads heads of head_dim (2 .. 256, even) elements; dt VX_F32 or VX_BF16,
+ * arithmetic in fp32.  y may be x itself (the same rows), but must not
+ * overlap it otherwise. */
+VX_API vx_status vx_rope_fwd(const vx_rows *x, const vx_rows *y, vx_dtype dt, int64_t n_tokens, int n_heads,
+                             int head_dim, const int64_t *pos, const vx_rope_cfg *rope, cudaStream_t stream);
+
+/* Writes the chunk's K and V ([n_tokens, n_kv_heads, head_dim] rows of the
+ * cache's dtype) to slots lens[s] + t of layer `layer`, zeroes acc there, and
+ * leaves lens and pos alone.  With rope (may be NULL), k is rotated at
+ * positions pos[s] + t on its way, and so is q (may be NULL; n_q_heads heads)
+ * into q_out (which may be q itself); without rope q must be NULL.  Rows must
+ * start on 16-byte boundaries.  Two sequences of one call must not append to
+ * the same page.  Workspace: 256 bytes (the status word). */
+VX_API vx_status vx_paged_append(const vx_paged_cache *cache, int layer, const vx_rope_cfg *rope, const vx_rows *q,
+                                 const vx_rows *q_out, int n_q_heads, const vx_rows *k, const vx_rows *v,
+                                 const int32_t *q_start, int64_t n_tokens, int max_q, void *ws, size_t ws_bytes,
+                                 cudaStream_t stream);
+
+/* lens[s] += n, pos[s] += n, n the rows of sequence s (see q_start above). */
+VX_API vx_status vx_paged_advance(const vx_paged_cache *cache, const int32_t *q_start, int64_t n_tokens, int max_q,
+                                  void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Scores and mask of vx_paged_attn_fwd.  Query t of sequence s sits at slot
+ * i = lens[s] + t and sees slot j < lens[s] + n iff
+ *   j < prefix[s]  or  i - window < j <= i      (window 0: all j <= i);
+ * prefix (device int32 [n_seqs], NULL = none) is a part that every query
+ * sees, also from before it: a prompt attended in both directions, or the
+ * first tokens kept in view of a sliding window.  Then
+ *   s = scale * q.k;  cap > 0: s = cap * tanh(s / cap);
+ *   slopes (device fp32 [n_q_heads], NULL = none): s -= slopes[h] * |i - j|.
+ * Distances count slots, so after an eviction they count the tokens kept.
+ * scale <= 0 selects 1 / sqrt(head_dim). */
+typedef struct vx_attn_opts {
+  float scale;
+  float cap;
+  int window;
+  const int32_t *prefix;
+  const float *slopes;
+} vx_attn_opts;
+
+/* Attention of a chunk of new tokens over the paged cache that already holds
+ * them (vx_paged_append): per query head h, o = softmax(s) v over the K/V head
+ * h / (n_q_heads / n_kv_heads), and lse (fp32 [n_tokens, n_q_heads], may be
+ * NULL) = log of the sum of exp(s).  A query that sees nothing gets zeros and
+ * lse -inf.  VX_BF16: tensor cores, fp32 softmax and sums; VX_F32: fp32
+ * throughout.
+ * q, o: rows of n_q_heads heads, dtype of the cache.  max_kv bounds lens[s] + n
+ * over the sequences (0 = max_pages * page_size; only the split of the work
+ * depends on it).  opts may be NULL (all zero).
+ * track != 0 adds up, per K/V head and slot j < lens[s] + n, the softmax
+ * weights that slot j got from the chunk's queries and the group's heads:
+ *   acc_j = track_decay * acc_j + sum      (track_decay 0 does not read acc).
+ * The sums' order is fixed, so equal calls give equal bits.
+ * K and V rows of slots that no query of the chunk sees may hold anything,
+ * infinities and NaN too; a non-finite V row that some query sees can reach
+ * the other queries of the same 256-row tile.
+ * Workspace: vx_paged_attn_workspace(). */
+VX_API vx_status vx_paged_attn_fwd(const vx_paged_cache *cache, int layer, const vx_rows *q, const vx_rows *o,
+                                   float *lse, int n_q_heads, const int32_t *q_start, int64_t n_tokens, int max_q,
+                                   int64_t max_kv, const vx_attn_opts *opts, int track, float track_decay, void *ws,
+                                   size_t ws_bytes, cudaStream_t stream);
+VX_API size_t vx_paged_attn_workspace(const vx_paged_cache *cache, int n_q_heads, int64_t n_tokens, int max_q,
+                                      int64_t max_kv, int want_lse, int track);
+
+/* Eviction: sequence s keeps, per layer and K/V head, its last r = min(recent,
+ * m) slots and of the others the m - r with the largest acc (ties: the lowest
+ * slot; NaN counts as lowest), m = min(keep, lens[s]), and they move, in slot
+ * order, to slots 0 .. m - 1 of dst, with their acc.  dst->lens[s] = m and
+ * dst->pos[s] = pos[s].  kept (may be NULL): the slots they came from,
+ * int32 [n_layers][n_seqs][n_kv_heads][keep], entries from m on untouched.
+ * dst is the cache itself (in place: pages from ceil(m / page_size) on are then
+ * free; no page may serve two sequences), or another cache of the same
+ * shape, dtype and page size (n_pages and max_pages may differ) none of whose
+ * pages the source uses.  Workspace: vx_paged_evict_workspace(). */
+VX_API vx_status vx_paged_evict(const vx_paged_cache *cache, const vx_paged_cache *dst, int64_t keep, int64_t recent,
+                                int32_t *kept, void *ws, size_t ws_bytes, cudaStream_t stream);
+VX_API size_t vx_paged_evict_workspace(const vx_paged_cache *cache, int64_t keep);
 
 /* Test hook for the bounded-wait machinery: launches one CTA that waits on an
  * mbarrier nothing arrives on, with a limit of timeout_ns, then records

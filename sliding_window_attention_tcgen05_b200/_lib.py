@@ -38,9 +38,30 @@ class VxKvRing(C.Structure):
                 ("n_streams", C.c_int), ("window", C.c_int)]
 
 
+class VxPagedCache(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("k", "v", "acc", "table", "lens", "pos")] + \
+               [(n, C.c_int) for n in ("dt", "n_layers", "n_pages", "page_size", "n_kv_heads", "head_dim", "n_seqs",
+                                       "max_pages")]
+
+
+class VxRows(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("row", C.c_int64), ("head", C.c_int64)]
+
+
+class VxRopeCfg(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("rot_dim", "interleaved", "scaling", "orig_len")] + \
+               [(n, C.c_double) for n in ("theta", "factor", "beta_fast", "beta_slow", "mscale")]
+
+
+class VxAttnOpts(C.Structure):
+    _fields_ = [("scale", C.c_float), ("cap", C.c_float), ("window", C.c_int), ("prefix", C.c_void_p),
+                ("slopes", C.c_void_p)]
+
+
 # name -> (restype, argtypes); this list is the exported ABI of include/vx.h.
 _P, _I, _F, _S, _U64, _I64 = C.c_void_p, C.c_int, C.c_float, C.c_size_t, C.c_uint64, C.c_int64
 _CFG, _W, _R = C.POINTER(VxLayerCfg), C.POINTER(VxLayerWeights), C.POINTER(VxKvRing)
+_PC, _RW, _RC, _AO = C.POINTER(VxPagedCache), C.POINTER(VxRows), C.POINTER(VxRopeCfg), C.POINTER(VxAttnOpts)
 SIGNATURES = {
     "vx_last_error": (C.c_char_p, []),
     "vx_version": (C.c_char_p, []),
@@ -71,6 +92,13 @@ SIGNATURES = {
     "vx_stream_prefill": (_I, [_CFG, _W, _R, _P, _P, _I, _P, _P, _S, _P]),
     "vx_stream_step": (_I, [_CFG, _W, _R, _P, _P, _I, _P, _P, _S, _P]),
     "vx_stream_step_workspace": (_S, [_CFG, _I, _I]),
+    "vx_rope_fwd": (_I, [_RW, _RW, _I, _I64, _I, _I, _P, _RC, _P]),
+    "vx_paged_append": (_I, [_PC, _I, _RC, _RW, _RW, _I, _RW, _RW, _P, _I64, _I, _P, _S, _P]),
+    "vx_paged_advance": (_I, [_PC, _P, _I64, _I, _P, _S, _P]),
+    "vx_paged_attn_fwd": (_I, [_PC, _I, _RW, _RW, _P, _I, _P, _I64, _I, _I64, _AO, _I, _F, _P, _S, _P]),
+    "vx_paged_attn_workspace": (_S, [_PC, _I, _I64, _I, _I64, _I, _I]),
+    "vx_paged_evict": (_I, [_PC, _PC, _I64, _I64, _P, _P, _S, _P]),
+    "vx_paged_evict_workspace": (_S, [_PC, _I64]),
     "vx_selftest_wait_timeout": (_I, [_P, _S, _U64, _P]),
 }
 

@@ -28,7 +28,9 @@
 #include <cudaTypedefs.h>
 
 #include "vx.h"
+#include "vx_api.h"
 #include "vx_internal.h"
+#include "vx_paged.h"
 
 namespace vx {
 
@@ -160,56 +162,6 @@ bool tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t ro
 using namespace vx;
 
 namespace {
-
-constexpr size_t kStatusBytes = 256;
-constexpr size_t kAlign = 1024;
-
-inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Bump allocator over the caller's workspace (or a size counter when base is null).
-struct Carve {
-  uint8_t* base;
-  size_t off;
-  void* take(size_t bytes) {
-    off = align_up(off, kAlign);
-    void* p = base ? base + off : nullptr;
-    off += bytes;
-    return p;
-  }
-};
-
-#define VX_CHECK_ARG(cond, ...)   \
-  do {                            \
-    if (!(cond)) {                \
-      set_error(__VA_ARGS__);     \
-      return VX_ERR_INVALID_ARG;  \
-    }                             \
-  } while (0)
-
-#define VX_CUDA(call)                                                          \
-  do {                                                                         \
-    cudaError_t e_ = (call);                                                   \
-    if (e_ != cudaSuccess) {                                                   \
-      set_error("%s failed: %s", #call, cudaGetErrorString(e_));               \
-      return VX_ERR_CUDA;                                                      \
-    }                                                                          \
-  } while (0)
-
-vx_status make_launch(Launch* L, void* ws, size_t ws_bytes, size_t need, cudaStream_t stream) {
-  VX_CHECK_ARG(ws != nullptr, "workspace is null");
-  VX_CHECK_ARG((reinterpret_cast<uintptr_t>(ws) & 255) == 0, "workspace must be 256-byte aligned");
-  VX_CHECK_ARG(ws_bytes >= need, "workspace too small: %zu bytes given, %zu needed", ws_bytes, need);
-  L->stream = stream;
-  L->status = static_cast<DevStatus*>(ws);
-  L->limit_ns = wait_limit_ns();
-  L->sm_count = current_sm_count();
-  if (L->sm_count <= 0) {
-    set_error("no CUDA device is current");
-    return VX_ERR_CUDA;
-  }
-  return VX_OK;
-}
 
 // A traced RMSNorm / partial-sum reduction launch (see launch_rmsnorm).
 cudaError_t rmsnorm(const Launch& L, const float* x, const float* parts, int nparts, int64_t part_stride,
@@ -628,6 +580,11 @@ vx_status vx_status_check(const void* ws, cudaStream_t stream) {
   if (h.code == kStatusTimeout) {
     set_error("a device-side wait expired (wait tag %d, block %u)", h.where, h.block);
     return VX_ERR_DEVICE_TIMEOUT;
+  }
+  if (h.code == kStatusBadCache) {
+    set_error("a paged-cache call met a page outside the pool or a sequence longer than its table (sequence %d)",
+              h.where);
+    return VX_ERR_INVALID_ARG;
   }
   return VX_OK;
 }

@@ -1,0 +1,110 @@
+// paged_attn.cuh -- what the attention kernels over the paged cache share: the
+// list of keys a block of queries sees, asynchronous row copies, the score
+// transform.
+//
+// A block of queries (tokens t_first .. t_last of one sequence) sees the slots
+// [0, pre) and [lo, hi).  They are walked as one list x = 0 .. total - 1: slot
+// j = x for x < pre, x + shift behind it (shift 0 when the two ranges touch).
+// In the list's coordinates token i sees x < pre or xlo(i) <= x <= xhi(i).
+#pragma once
+
+#include "vx_paged.h"
+
+namespace vx {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kNoWindow = 1 << 30;
+
+struct KeyList {
+  int pre, shift, total;
+};
+
+__device__ __forceinline__ KeyList key_list(int i_first, int i_last, int window, int prefix, int kv) {
+  KeyList k;
+  const int lo = min(max(0, i_first - window + 1), kv);
+  const int hi = min(i_last + 1, kv);
+  k.pre = min(max(prefix, 0), kv);
+  if (k.pre >= lo) {
+    k.shift = 0;
+    k.total = max(hi, k.pre);
+  } else {
+    k.shift = lo - k.pre;
+    k.total = k.pre + max(hi - lo, 0);
+  }
+  return k;
+}
+__device__ __forceinline__ int key_slot(const KeyList& k, int x) { return x + (x >= k.pre ? k.shift : 0); }
+
+// 16 bytes global -> shared, or zeros when !valid (src must be readable all the same: it is not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr));
+}
+// D = A(16x16, row) * B(16x8, col) + D, bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Scores to the exponent's base-2 units.  Without cap and slopes that is one
+// multiplication by scale * log2(e).  cap * tanh(z) = cap * (1 - 2 / (e^{2z} + 1)),
+// from one exponential and one reciprocal (absolute error about cap * 2^-23,
+// where the hardware's own tanh would leave cap * 2^-11).
+struct ScoreMod {
+  float sl2;       // scale * log2 e
+  float cap2;      // cap * log2 e, 0 = no cap
+  float two_z;     // 2 scale / cap * log2 e
+};
+__device__ __forceinline__ ScoreMod score_mod(const PagedAttnArgs& a) {
+  ScoreMod m;
+  m.sl2 = a.scale * kLog2e;
+  m.cap2 = a.cap * kLog2e;
+  m.two_z = a.cap > 0.f ? 2.f * a.scale / a.cap * kLog2e : 0.f;
+  return m;
+}
+// slope2 = slope of the head * log2 e, dist = |i - j|
+__device__ __forceinline__ float score2(const ScoreMod& m, float s, float slope2, int dist) {
+  float y;
+  if (m.cap2 > 0.f) {
+    const float e = ex2_approx(s * m.two_z);
+    y = m.cap2 - 2.f * m.cap2 * rcp_approx(e + 1.f);
+  } else {
+    y = s * m.sl2;
+  }
+  return y - slope2 * static_cast<float>(dist);
+}
+
+cudaError_t launch_paged_attn_rows(const Launch& L, const PagedAttnArgs& a);
+cudaError_t launch_paged_attn_tc(const Launch& L, const PagedAttnArgs& a);
+cudaError_t launch_paged_attn_f32(const Launch& L, const PagedAttnArgs& a);
+cudaError_t launch_paged_attn_combine(const Launch& L, const PagedAttnArgs& a, bool bf16);
+cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, bool bf16, int64_t max_kv);
+
+constexpr int kMaxSplits = 64;
+
+}  // namespace vx

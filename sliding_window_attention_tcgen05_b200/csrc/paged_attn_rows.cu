@@ -1,0 +1,715 @@
+// paged_attn_rows.cu -- attention over the paged cache for few query rows
+// (decoding, streaming steps), its fp32 form, the joining of split key ranges
+// and the accumulated attention weights.
+#include "paged_attn.cuh"
+
+namespace vx {
+
+namespace {
+
+// paged_attn_rows_kernel: CTA per (key range, K/V head, sequence), four warps.
+// The up to 16 * MT query rows (token t, head g of the group: row t * G + g)
+// are the M side of mma.sync tiles, so one read of a K/V row serves the whole
+// group; tcgen05's M >= 64 tiles would be mostly padding.  Each warp walks its
+// own tiles of KT keys through its own ring of cp.async stages (no CTA barrier
+// in the loop), with the page of every row looked up one tile ahead; the four
+// warps' softmax states are joined through shared memory at the end.
+constexpr int kRowsThreads = 128;
+constexpr int kRowsStages = 3;
+constexpr int kRowsStageBytes = 8192;   // K and V of one warp tile
+
+template <int D, int MT, bool MOD>
+__global__ void __launch_bounds__(kRowsThreads)
+paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int KT = kRowsStageBytes / (4 * D);   // 16 keys (D 128) or 32 (D 64)
+  constexpr int CPR = D / 8;                      // 16-byte chunks of a row
+  constexpr int RPI = 32 / CPR;                   // rows per warp-wide copy
+  constexpr int ROWS = 16 * MT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int sp = blockIdx.x, kh = blockIdx.y, s = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SeqSpan q = seq_span(a.c, a.ch, s);
+  if (q.n <= 0) return;
+  if (q.over && threadIdx.x == 0) report_bad_cache(a.status, s);
+  const int G = a.group, rows = q.n * G;
+  const KeyList kl = key_list(q.old, q.old + q.n - 1, a.window, a.prefix ? a.prefix[s] : 0, q.kv);
+  const int step = ((kl.total + a.splits - 1) / a.splits + KT - 1) / KT * KT;
+  const int x0 = min(sp * step, kl.total), x1 = min(x0 + step, kl.total);
+  const int tiles = (x1 - x0 + KT - 1) / KT;
+  const int mine = tiles > warp ? (tiles - warp + 3) / 4 : 0;
+
+  uint8_t* stage_base = smem + warp * kRowsStages * kRowsStageBytes;
+  const uint32_t stage_addr = smem_addr(stage_base);
+  const uint16_t* kp = static_cast<const uint16_t*>(a.k);
+  const uint16_t* vp = static_cast<const uint16_t*>(a.v);
+
+  const int lrow = lane & (KT - 1);
+  auto lookup = [&](int i) -> int64_t {   // this lane's row of the warp's tile i, or -1
+    const int x = x0 + (warp + 4 * i) * KT + lrow;
+    if (i >= mine || x >= x1) return -1;
+    const int64_t r = slot_row(a.c, s, kh, key_slot(kl, x));
+    if (r < 0) report_bad_cache(a.status, s);
+    return r;
+  };
+  auto issue = [&](int i, int64_t row) {
+    if (i < mine) {
+      const uint32_t st = stage_addr + (i % kRowsStages) * kRowsStageBytes;
+#pragma unroll
+      for (int it = 0; it < KT / RPI; ++it) {
+        const int r = it * RPI + lane / CPR, c = lane % CPR;
+        const int64_t gr = __shfl_sync(0xffffffffu, row, r);
+        const int64_t e = (gr < 0 ? 0 : gr) * D + c * 8;
+        const uint32_t dst = st + r * (2 * D) + ((c ^ (r & 7)) << 4);
+        cp_async16(dst, kp + e, gr >= 0);
+        cp_async16(dst + kRowsStageBytes / 2, vp + e, gr >= 0);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRowsStages - 1; ++i) issue(i, lookup(i));
+  int64_t next_row = lookup(kRowsStages - 1);
+
+  // Query fragments (A operand) and each row's place: rows lane / 4 and + 8 of every 16-row tile.
+  const int qr = lane >> 2, qc = (lane & 3) * 2;
+  uint32_t qa[MT][D / 16][4];
+  int xlo[MT][2], xhi[MT][2], qi[MT][2];
+  float slope2[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = mt * 16 + half * 8 + qr;
+      const bool ok = r < rows;
+      const int t = a.group_div.div(ok ? r : 0), g = (ok ? r : 0) - t * G;
+      const int i = q.old + t;
+      qi[mt][half] = i;
+      xlo[mt][half] = max(0, i - a.window + 1 - kl.shift);
+      xhi[mt][half] = i - kl.shift;
+      slope2[mt][half] = MOD && a.slopes ? a.slopes[kh * G + g] * kLog2e : 0.f;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q.p) + (q.row0 + t) * a.q.row + (kh * G + g) * a.q.head;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qa[mt][ks][half] = ok ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + qc) : 0u;
+        qa[mt][ks][half + 2] = ok ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + qc) : 0u;
+      }
+    }
+  const ScoreMod sm = score_mod(a);
+  const int pre = min(kl.pre, x1);
+  // Tiles inside [all_lo, all_hi] or below pre need no mask.
+  const int all_lo = max(0, q.old + q.n - 1 - a.window + 1 - kl.shift), all_hi = min(q.old - kl.shift, x1 - 1);
+
+  float o[MT][D / 8][4];
+  float m_run[MT][2], l_part[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    m_run[mt][0] = m_run[mt][1] = -INFINITY;
+    l_part[mt][0] = l_part[mt][1] = 0.f;
+#pragma unroll
+    for (int nb = 0; nb < D / 8; ++nb) o[mt][nb][0] = o[mt][nb][1] = o[mt][nb][2] = o[mt][nb][3] = 0.f;
+  }
+
+  for (int i = 0; i < mine; ++i) {
+    cp_async_wait<kRowsStages - 2>();
+    __syncwarp();
+    {   // the stage read in the last turn is free again
+      const int64_t row = next_row;
+      next_row = lookup(i + kRowsStages);
+      issue(i + kRowsStages - 1, row);
+    }
+    const uint32_t kb = stage_addr + (i % kRowsStages) * kRowsStageBytes, vb = kb + kRowsStageBytes / 2;
+    const int xt = x0 + (warp + 4 * i) * KT;
+#pragma unroll
+    for (int b = 0; b < KT / 16; ++b) {
+      const int xb = xt + b * 16;
+      if (xb >= x1) break;
+      float sa[MT][2][4];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) sa[mt][nb][0] = sa[mt][nb][1] = sa[mt][nb][2] = sa[mt][nb][3] = 0.f;
+        const int kr = b * 16 + nb * 8 + (lane & 7);
+#pragma unroll
+        for (int h = 0; h < D / 32; ++h) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(kb + kr * (2 * D) + (((h * 4 + (lane >> 3)) ^ (kr & 7)) << 4), b0, b1, b2, b3);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma_bf16_16816(sa[mt][nb], qa[mt][2 * h][0], qa[mt][2 * h][1], qa[mt][2 * h][2], qa[mt][2 * h][3], b0, b1);
+            mma_bf16_16816(sa[mt][nb], qa[mt][2 * h + 1][0], qa[mt][2 * h + 1][1], qa[mt][2 * h + 1][2],
+                           qa[mt][2 * h + 1][3], b2, b3);
+          }
+        }
+      }
+      const bool clean = (xb >= all_lo && xb + 15 <= all_hi) || xb + 15 < pre;
+      uint32_t pa[MT][4];
+      bool grew = false;
+      float alpha[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float cmax = -INFINITY;
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& v = sa[mt][nb][2 * half + e];
+              const int x = xb + nb * 8 + qc + e;
+              v = MOD ? score2(sm, v, slope2[mt][half], abs(qi[mt][half] - key_slot(kl, x))) : v * sm.sl2;
+              if (!clean) v = (x < pre || (x >= xlo[mt][half] && x <= xhi[mt][half] && x < x1)) ? v : -INFINITY;
+              cmax = fmaxf(cmax, v);
+            }
+          cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, 1));
+          cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, 2));
+          const float m_new = fmaxf(m_run[mt][half], cmax);
+          const float mu = m_new == -INFINITY ? 0.f : m_new;
+          alpha[mt][half] = ex2_approx(m_run[mt][half] - mu);
+          grew |= m_new != m_run[mt][half];
+          m_run[mt][half] = m_new;
+          float p[2][2];
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[nb][e] = ex2_approx(sa[mt][nb][2 * half + e] - mu);
+          l_part[mt][half] = l_part[mt][half] * alpha[mt][half] + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
+          pa[mt][half] = pack_bf16x2(p[0][0], p[0][1]);
+          pa[mt][half + 2] = pack_bf16x2(p[1][0], p[1][1]);
+        }
+      if (__any_sync(0xffffffffu, grew)) {   // alpha is 1 for every row otherwise
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nb = 0; nb < D / 8; ++nb) {
+            o[mt][nb][0] *= alpha[mt][0];
+            o[mt][nb][1] *= alpha[mt][0];
+            o[mt][nb][2] *= alpha[mt][1];
+            o[mt][nb][3] *= alpha[mt][1];
+          }
+      }
+      const int vr = b * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int dc = 0; dc < D / 8; dc += 2) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_t(vb + vr * (2 * D) + (((dc + (lane >> 4)) ^ (vr & 7)) << 4), b0, b1, b2, b3);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma_bf16_16816(o[mt][dc], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b0, b1);
+          mma_bf16_16816(o[mt][dc + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b2, b3);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+
+  // Join the four warps (the stages are free once all of them are here).
+  float* sm_m = reinterpret_cast<float*>(smem);          // [4][ROWS]
+  float* sm_l = sm_m + 4 * ROWS;                         // [4][ROWS]
+  float* sm_o = sm_l + 4 * ROWS;                         // [4][ROWS][D]
+  __syncthreads();
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float l = l_part[mt][half];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const int r = mt * 16 + half * 8 + qr;
+      if (r < rows) {
+        if ((lane & 3) == 0) {
+          sm_m[warp * ROWS + r] = m_run[mt][half];
+          sm_l[warp * ROWS + r] = l;
+        }
+#pragma unroll
+        for (int nb = 0; nb < D / 8; ++nb)
+          *reinterpret_cast<float2*>(sm_o + (warp * ROWS + r) * D + nb * 8 + qc) =
+              make_float2(o[mt][nb][2 * half], o[mt][nb][2 * half + 1]);
+      }
+    }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < rows * (D / 2); idx += kRowsThreads) {
+    const int r = idx / (D / 2), d = (idx % (D / 2)) * 2;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w * ROWS + r]);
+    float l = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (sm_l[w * ROWS + r] == 0.f) continue;   // the warp saw no key (a NaN score leaves a NaN sum)
+      const float f = ex2_approx(sm_m[w * ROWS + r] - M);
+      const float2 y = *reinterpret_cast<const float2*>(sm_o + (w * ROWS + r) * D + d);
+      l = fmaf(sm_l[w * ROWS + r], f, l);
+      y0 = fmaf(y.x, f, y0);
+      y1 = fmaf(y.y, f, y1);
+    }
+    const int t = a.group_div.div(r), h = kh * G + r - t * G;
+    const int64_t tok = q.row0 + t;
+    if (a.splits > 1) {
+      const int64_t pr = (static_cast<int64_t>(sp) * a.ch.n_tokens + tok) * a.n_q_heads + h;
+      if (l != 0.f) *reinterpret_cast<float2*>(a.part_o + pr * D + d) = make_float2(y0, y1);
+      if (d == 0) a.part_ml[pr] = make_float2(M, l);
+    } else {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + tok * a.o_row + h * a.o_head + d) =
+          pack_bf16x2(y0 * inv, y1 * inv);
+      if (d == 0 && a.lse) a.lse[tok * a.n_q_heads + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- fp32 --
+// paged_attn_f32_kernel: CTA per (16-row block x key range, K/V head,
+// sequence), four warps of four rows each; 32-key tiles of K (padded rows) and
+// V in shared memory, scores with one key per lane, P V with D / 32 dims per
+// lane.  CUDA cores throughout: tensor-core tf32 would keep 10 mantissa bits.
+constexpr int kF32Rows = 16;
+constexpr int kF32Keys = 32;
+
+template <int D>
+__global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int KP = D + 4;        // padded K row: 16-byte reads of 32 rows hit all banks evenly
+  constexpr int V = D / 32;
+  __shared__ __align__(16) float sq[kF32Rows][D];
+  __shared__ __align__(16) float sk[kF32Keys][KP];
+  __shared__ __align__(16) float sv[kF32Keys][D];
+  __shared__ __align__(16) float spr[kF32Rows][kF32Keys];
+  const int rb = blockIdx.x % blocks, sp = blockIdx.x / blocks, kh = blockIdx.y, s = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SeqSpan q = seq_span(a.c, a.ch, s);
+  const int G = a.group, rows = q.n * G, r0 = rb * kF32Rows;
+  if (r0 >= rows) return;
+  if (q.over && threadIdx.x == 0) report_bad_cache(a.status, s);
+  const int rn = min(kF32Rows, rows - r0);
+  const int tf = a.group_div.div(r0), tl = a.group_div.div(r0 + rn - 1);
+  const KeyList kl = key_list(q.old + tf, q.old + tl, a.window, a.prefix ? a.prefix[s] : 0, q.kv);
+  const int step = ((kl.total + a.splits - 1) / a.splits + kF32Keys - 1) / kF32Keys * kF32Keys;
+  const int x0 = min(sp * step, kl.total), x1 = min(x0 + step, kl.total);
+  const float* kp = static_cast<const float*>(a.k);
+  const float* vp = static_cast<const float*>(a.v);
+  for (int i = threadIdx.x; i < kF32Rows * (D / 4); i += 128) {
+    const int r = i / (D / 4), c = i % (D / 4);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rn) {
+      const int t = a.group_div.div(r0 + r), h = kh * G + r0 + r - t * G;
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head +
+                                           c * 4);
+    }
+    *reinterpret_cast<float4*>(&sq[r][c * 4]) = x;
+  }
+  const ScoreMod sm = score_mod(a);
+  int qi[4];
+  float slope2[4], m[4], l[4], acc[4][V];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = min(r0 + warp * 4 + j, rows - 1);
+    const int t = a.group_div.div(r);
+    qi[j] = q.old + t;
+    slope2[j] = a.slopes ? a.slopes[kh * G + r - t * G] * kLog2e : 0.f;
+    m[j] = -INFINITY;
+    l[j] = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[j][e] = 0.f;
+  }
+  for (int xt = x0; xt < x1; xt += kF32Keys) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kF32Keys * (D / 4); i += 128) {
+      const int r = i / (D / 4), c = i % (D / 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (xt + r < x1) {
+        const int64_t gr = slot_row(a.c, s, kh, key_slot(kl, xt + r));
+        if (gr >= 0) {
+          x = *reinterpret_cast<const float4*>(kp + gr * D + c * 4);
+          y = *reinterpret_cast<const float4*>(vp + gr * D + c * 4);
+        } else {
+          report_bad_cache(a.status, s);
+        }
+      }
+      *reinterpret_cast<float4*>(&sk[r][c * 4]) = x;
+      *reinterpret_cast<float4*>(&sv[r][c * 4]) = y;
+    }
+    __syncthreads();
+    float dot[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int c = 0; c < D / 4; ++c) {
+      const float4 kk = *reinterpret_cast<const float4*>(&sk[lane][c * 4]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 qq = *reinterpret_cast<const float4*>(&sq[warp * 4 + j][c * 4]);
+        dot[j] = fmaf(qq.x, kk.x, dot[j]);
+        dot[j] = fmaf(qq.y, kk.y, dot[j]);
+        dot[j] = fmaf(qq.z, kk.z, dot[j]);
+        dot[j] = fmaf(qq.w, kk.w, dot[j]);
+      }
+    }
+    const int x = xt + lane, js = key_slot(kl, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool seen = x < x1 && (js < kl.pre || (js <= qi[j] && js > qi[j] - a.window));
+      const float v = seen ? score2(sm, dot[j], slope2[j], abs(qi[j] - js)) : -INFINITY;
+      float cmax = v;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, off));
+      const float m_new = fmaxf(m[j], cmax);
+      const float mu = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m[j] - mu);
+      const float p = exp2f(v - mu);
+      float ps = p;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
+      m[j] = m_new;
+      l[j] = l[j] * alpha + ps;
+      spr[warp * 4 + j][lane] = p;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[j][e] *= alpha;
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int kk = 0; kk < kF32Keys; ++kk) {
+      float vv[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) vv[e] = sv[kk][lane * V + e];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = spr[warp * 4 + j][kk];
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[j][e] = fmaf(p, vv[e], acc[j][e]);
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = r0 + warp * 4 + j;
+    if (r >= rows) continue;
+    const int t = a.group_div.div(r), h = kh * G + r - t * G;
+    const int64_t tok = q.row0 + t;
+    if (a.splits > 1) {
+      const int64_t pr = (static_cast<int64_t>(sp) * a.ch.n_tokens + tok) * a.n_q_heads + h;
+#pragma unroll
+      for (int e = 0; e < V; ++e) a.part_o[pr * D + lane * V + e] = acc[j][e];
+      if (lane == 0) a.part_ml[pr] = make_float2(m[j], l[j]);
+    } else {
+      const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
+      float* dst = static_cast<float*>(a.o) + tok * a.o_row + h * a.o_head;
+#pragma unroll
+      for (int e = 0; e < V; ++e) dst[lane * V + e] = acc[j][e] * inv;
+      if (lane == 0 && a.lse) a.lse[tok * a.n_q_heads + h] = l[j] == 0.f ? -INFINITY : (m[j] + log2f(l[j])) * kLn2;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- combine --
+// One warp per (token, head): the parts' maxima and sums, then the weighted
+// sum of their outputs, D / 32 elements per lane.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int64_t tok = row / a.n_q_heads;
+  const int h = static_cast<int>(row - tok * a.n_q_heads);
+  // Rows outside every sequence (or past max_q) have no parts: find the row's sequence.
+  int lo = 0, hi = a.c.n_seqs;   // last s with q_start[s] <= tok
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.ch.q_start[mid] <= tok) lo = mid; else hi = mid;
+  }
+  const SeqSpan q = seq_span(a.c, a.ch, lo);
+  if (tok < q.row0 || tok >= q.row0 + q.n) return;
+  float2 ml[kMaxSplits / 32];
+  float M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 32; ++i) {
+    const int sp = i * 32 + lane;
+    ml[i] = sp < a.splits ? a.part_ml[sp * rows + row] : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, ml[i].x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float l = 0.f, w[kMaxSplits / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 32; ++i) {
+    w[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - M);
+    l += ml[i].y * w[i];
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  float y[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) y[e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 32; ++i)
+#pragma unroll 4
+    for (int j = 0; j < 32; ++j) {
+      const int sp = i * 32 + j;
+      if (sp >= a.splits) break;
+      const float ws = __shfl_sync(0xffffffffu, w[i], j);
+      if (ws == 0.f) continue;   // an empty part wrote no output
+      const float* src = a.part_o + (sp * rows + row) * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = fmaf(src[e], ws, y[e]);
+    }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if constexpr (BF16) {
+    uint16_t* dst = static_cast<uint16_t*>(a.o) + tok * a.o_row + h * a.o_head + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(y[e] * inv, y[e + 1] * inv);
+  } else {
+    float* dst = static_cast<float*>(a.o) + tok * a.o_row + h * a.o_head + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) dst[e] = y[e] * inv;
+  }
+  if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- weights --
+// Accumulated weights: acc_j = decay * acc_j + sum over the chunk's rows of
+// exp(s - lse).  The keys are the M side (K fragments stay in registers), the
+// rows stream past in blocks of 64, so every slot's sum stays in one thread
+// group's registers: no atomics, a fixed order.
+constexpr int kWKeys = 64;
+constexpr int kWRows = 64;
+
+template <int D, bool MOD>
+__global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_constant__ PagedAttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int CPR = D / 8;
+  extern __shared__ __align__(128) uint8_t smem[];   // K tile, two Q blocks of 64 rows, their places
+  const uint32_t sk = smem_addr(smem);
+  const uint32_t sq0 = sk + kWKeys * 2 * D;
+  float* s_lse = reinterpret_cast<float*>(smem + (kWKeys + 2 * kWRows) * 2 * D);   // [2][64]
+  int* s_i = reinterpret_cast<int*>(s_lse + 2 * kWRows);                          // [2][64]
+  float* s_sl = reinterpret_cast<float*>(s_i + 2 * kWRows);                       // [2][64]
+  const int kh = blockIdx.y, s = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const SeqSpan q = seq_span(a.c, a.ch, s);
+  if (q.n <= 0) return;
+  const int G = a.group;
+  const int pre = min(a.prefix ? max(a.prefix[s], 0) : 0, q.kv);
+  const ScoreMod sm = score_mod(a);
+  const uint16_t* kp = static_cast<const uint16_t*>(a.k);
+  const uint16_t* qp = static_cast<const uint16_t*>(a.q.p);
+  for (int tile = blockIdx.x; tile * kWKeys < q.kv; tile += gridDim.x) {
+    const int j0 = tile * kWKeys, j1 = min(j0 + kWKeys, q.kv);
+    // Tokens that see some slot of the tile.
+    int t0 = max(0, j0 - q.old);
+    int t1 = min(q.n, j1 - 1 - q.old + min(a.window, kNoWindow - 1 - j1));
+    if (j0 < pre) { t0 = 0; t1 = q.n; }
+    const int ra = t0 * G, rz = max(t1 * G, ra);
+    auto stage_q = [&](int blk, int buf) {
+      const int rbase = ra + blk * kWRows;
+      for (int i = tid; i < kWRows * CPR; i += 128) {
+        const int r = i / CPR, c = i % CPR;
+        const bool ok = rbase + r < rz;
+        const int t = a.group_div.div(ok ? rbase + r : 0), h = kh * G + (ok ? rbase + r : 0) - t * G;
+        cp_async16(sq0 + buf * kWRows * 2 * D + r * 2 * D + ((c ^ (r & 7)) << 4),
+                   qp + (q.row0 + t) * a.q.row + h * a.q.head + c * 8, ok);
+      }
+      if (tid < kWRows) {
+        const bool ok = rbase + tid < rz;
+        const int t = a.group_div.div(ok ? rbase + tid : 0), h = kh * G + (ok ? rbase + tid : 0) - t * G;
+        const float z = ok ? a.lse[static_cast<int64_t>(q.row0 + t) * a.n_q_heads + h] : -INFINITY;
+        s_lse[buf * kWRows + tid] = z == -INFINITY ? INFINITY : z * kLog2e;   // weight 0 without a sum
+        s_i[buf * kWRows + tid] = q.old + t;
+        s_sl[buf * kWRows + tid] = a.slopes ? a.slopes[h] * kLog2e : 0.f;
+      }
+      cp_async_commit();
+    };
+    const int blocks = (rz - ra + kWRows - 1) / kWRows;
+    for (int i = tid; i < kWKeys * CPR; i += 128) {
+      const int r = i / CPR, c = i % CPR;
+      const int64_t gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
+      cp_async16(sk + r * 2 * D + ((c ^ (r & 7)) << 4), kp + (gr < 0 ? 0 : gr) * D + c * 8, gr >= 0);
+    }
+    if (blocks > 0) stage_q(0, 0); else cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    // This warp's 16 keys as A fragments: ldmatrix x4 = rows 0-7 / 8-15 at dims 0-7 / 8-15.
+    uint32_t ka[D / 16][4];
+    {
+      const int r = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        ldsm_x4(sk + r * 2 * D + (((ks * 2 + (lane >> 4)) ^ (r & 7)) << 4), ka[ks][0], ka[ks][1], ka[ks][2], ka[ks][3]);
+    }
+    const int jr[2] = {j0 + warp * 16 + (lane >> 2), j0 + warp * 16 + (lane >> 2) + 8};
+    float sum[2] = {0.f, 0.f};
+    for (int blk = 0; blk < blocks; ++blk) {
+      const int buf = blk & 1;
+      if (blk > 0) {
+        cp_async_wait<0>();
+        __syncthreads();
+      }
+      if (blk + 1 < blocks) stage_q(blk + 1, buf ^ 1);
+      const uint32_t sq = sq0 + buf * kWRows * 2 * D;
+#pragma unroll 2
+      for (int nb = 0; nb < kWRows / 8; ++nb) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        const int r = nb * 8 + (lane & 7);
+#pragma unroll
+        for (int h = 0; h < D / 32; ++h) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(sq + r * 2 * D + (((h * 4 + (lane >> 3)) ^ (r & 7)) << 4), b0, b1, b2, b3);
+          mma_bf16_16816(c, ka[2 * h][0], ka[2 * h][1], ka[2 * h][2], ka[2 * h][3], b0, b1);
+          mma_bf16_16816(c, ka[2 * h + 1][0], ka[2 * h + 1][1], ka[2 * h + 1][2], ka[2 * h + 1][3], b2, b3);
+        }
+        const int col = buf * kWRows + nb * 8 + (lane & 3) * 2;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float z = s_lse[col + e];
+          const int i = s_i[col + e];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int j = jr[half];
+            const float v = MOD ? score2(sm, c[2 * half + e], s_sl[col + e], abs(i - j)) : c[2 * half + e] * sm.sl2;
+            const bool seen = j < pre || (j <= i && j > i - a.window);
+            sum[half] += seen ? ex2_approx(v - z) : 0.f;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float x = sum[half];
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      if ((lane & 3) == 0 && jr[half] < j1) {
+        const int64_t row = slot_row(a.c, s, kh, jr[half]);
+        if (row >= 0) a.acc[row] = (a.acc_decay != 0.f ? a.acc_decay * a.acc[row] : 0.f) + x;
+      }
+    }
+    __syncthreads();   // the tile's buffers are refilled
+  }
+}
+
+// fp32: CTA per 32 slots; a lane owns a slot, each warp every fourth row.
+template <int D>
+__global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __grid_constant__ PagedAttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int KP = D + 4;
+  __shared__ __align__(16) float sk[32][KP];
+  __shared__ __align__(16) float sq[4][D];
+  __shared__ float part[4][32];
+  const int kh = blockIdx.y, s = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const SeqSpan q = seq_span(a.c, a.ch, s);
+  if (q.n <= 0) return;
+  const int G = a.group;
+  const int pre = min(a.prefix ? max(a.prefix[s], 0) : 0, q.kv);
+  const ScoreMod sm = score_mod(a);
+  for (int tile = blockIdx.x; tile * 32 < q.kv; tile += gridDim.x) {
+    const int j0 = tile * 32, j1 = min(j0 + 32, q.kv);
+    __syncthreads();
+    for (int i = tid; i < 32 * (D / 4); i += 128) {
+      const int r = i / (D / 4), c = i % (D / 4);
+      const int64_t gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
+      *reinterpret_cast<float4*>(&sk[r][c * 4]) =
+          gr >= 0 ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + gr * D + c * 4)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+    const int j = j0 + lane;
+    int t0 = max(0, j0 - q.old), t1 = min(q.n, j1 - 1 - q.old + min(a.window, kNoWindow - 1 - j1));
+    if (j0 < pre) { t0 = 0; t1 = q.n; }
+    float sum = 0.f;
+    for (int r = t0 * G + warp; r < t1 * G; r += 4) {
+      const int t = a.group_div.div(r), h = kh * G + r - t * G;
+      const float* src = static_cast<const float*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head;
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) sq[warp][e * 32 + lane] = src[e * 32 + lane];
+      __syncwarp();
+      float dot = 0.f;
+#pragma unroll 8
+      for (int c = 0; c < D / 4; ++c) {
+        const float4 kk = *reinterpret_cast<const float4*>(&sk[lane][c * 4]);
+        const float4 qq = *reinterpret_cast<const float4*>(&sq[warp][c * 4]);
+        dot = fmaf(qq.x, kk.x, dot);
+        dot = fmaf(qq.y, kk.y, dot);
+        dot = fmaf(qq.z, kk.z, dot);
+        dot = fmaf(qq.w, kk.w, dot);
+      }
+      const int i = q.old + t;
+      const float z = a.lse[static_cast<int64_t>(q.row0 + t) * a.n_q_heads + h];
+      const bool seen = z != -INFINITY && (j < pre || (j <= i && j > i - a.window));
+      const float v = score2(sm, dot, a.slopes ? a.slopes[h] * kLog2e : 0.f, abs(i - j));
+      sum += seen ? exp2f(v - z * kLog2e) : 0.f;
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && j < j1) {
+      const int64_t row = slot_row(a.c, s, kh, j);
+      const float x = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+      if (row >= 0) a.acc[row] = (a.acc_decay != 0.f ? a.acc_decay * a.acc[row] : 0.f) + x;
+    }
+  }
+}
+
+template <int D, int MT, bool MOD>
+cudaError_t launch_rows(const Launch& L, const PagedAttnArgs& a) {
+  constexpr size_t ring = 4 * kRowsStages * kRowsStageBytes;
+  constexpr size_t join = (2 * 4 * 16 * MT + 4 * 16 * MT * D) * sizeof(float);
+  constexpr size_t smem = ring > join ? ring : join;
+  const dim3 grid(a.splits, a.c.n_heads, a.c.n_seqs);
+  return launch_kernel(paged_attn_rows_kernel<D, MT, MOD>, grid, dim3(kRowsThreads), smem, L.stream, a);
+}
+template <int D>
+cudaError_t launch_rows_d(const Launch& L, const PagedAttnArgs& a) {
+  const bool mod = a.cap > 0.f || a.slopes != nullptr;
+  if (a.ch.max_q * a.group <= 16) return mod ? launch_rows<D, 1, true>(L, a) : launch_rows<D, 1, false>(L, a);
+  return mod ? launch_rows<D, 2, true>(L, a) : launch_rows<D, 2, false>(L, a);
+}
+
+template <int D, bool MOD>
+cudaError_t launch_weights(const Launch& L, const PagedAttnArgs& a, int64_t max_kv) {
+  constexpr size_t smem = (kWKeys + 2 * kWRows) * 2 * D + 3 * 2 * kWRows * 4;
+  const dim3 grid(static_cast<unsigned>((max_kv + kWKeys - 1) / kWKeys), a.c.n_heads, a.c.n_seqs);
+  return launch_kernel(paged_attn_weights_kernel<D, MOD>, grid, dim3(128), smem, L.stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn_rows(const Launch& L, const PagedAttnArgs& a) {
+  return a.head_dim == 128 ? launch_rows_d<128>(L, a) : launch_rows_d<64>(L, a);
+}
+
+cudaError_t launch_paged_attn_f32(const Launch& L, const PagedAttnArgs& a) {
+  const int blocks = static_cast<int>((static_cast<int64_t>(a.ch.max_q) * a.group + kF32Rows - 1) / kF32Rows);
+  const dim3 grid(static_cast<unsigned>(blocks) * a.splits, a.c.n_heads, a.c.n_seqs);
+  return a.head_dim == 128 ? launch_kernel(paged_attn_f32_kernel<128>, grid, dim3(128), 0, L.stream, a, blocks)
+                           : launch_kernel(paged_attn_f32_kernel<64>, grid, dim3(128), 0, L.stream, a, blocks);
+}
+
+cudaError_t launch_paged_attn_combine(const Launch& L, const PagedAttnArgs& a, bool bf16) {
+  const int64_t rows = static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
+  const dim3 grid(static_cast<unsigned>((rows + 3) / 4)), block(128);
+  if (a.head_dim == 128)
+    return bf16 ? launch_kernel(paged_attn_combine_kernel<128, true>, grid, block, 0, L.stream, a)
+                : launch_kernel(paged_attn_combine_kernel<128, false>, grid, block, 0, L.stream, a);
+  return bf16 ? launch_kernel(paged_attn_combine_kernel<64, true>, grid, block, 0, L.stream, a)
+              : launch_kernel(paged_attn_combine_kernel<64, false>, grid, block, 0, L.stream, a);
+}
+
+cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, bool bf16, int64_t max_kv) {
+  const bool mod = a.cap > 0.f || a.slopes != nullptr;
+  if (!bf16) {
+    const dim3 grid(static_cast<unsigned>((max_kv + 31) / 32), a.c.n_heads, a.c.n_seqs);
+    return a.head_dim == 128 ? launch_kernel(paged_attn_weights_f32_kernel<128>, grid, dim3(128), 0, L.stream, a)
+                             : launch_kernel(paged_attn_weights_f32_kernel<64>, grid, dim3(128), 0, L.stream, a);
+  }
+  if (a.head_dim == 128)
+    return mod ? launch_weights<128, true>(L, a, max_kv) : launch_weights<128, false>(L, a, max_kv);
+  return mod ? launch_weights<64, true>(L, a, max_kv) : launch_weights<64, false>(L, a, max_kv);
+}
+
+}  // namespace vx

@@ -24,26 +24,25 @@ __device__ __forceinline__ float2 rope_cs(int64_t pos, uint64_t turns, float msc
   return make_float2(c * mscale, s * mscale);
 }
 
+// Eight bf16 or four fp32 elements: one 16-byte access, widened to fp32 and back.
 template <bool BF16>
-struct Vec {   // one 16-byte access
+struct Vec {
   static constexpr int N = BF16 ? 8 : 4;
   float f[N];
-  __device__ __forceinline__ void load(const void* p) {
+  __device__ __forceinline__ explicit Vec(const uint4& a) {
     if constexpr (BF16) {
-      const uint4 a = *static_cast<const uint4*>(p);
       f[0] = bf16lo(a.x); f[1] = bf16hi(a.x); f[2] = bf16lo(a.y); f[3] = bf16hi(a.y);
       f[4] = bf16lo(a.z); f[5] = bf16hi(a.z); f[6] = bf16lo(a.w); f[7] = bf16hi(a.w);
     } else {
-      const float4 a = *static_cast<const float4*>(p);
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
     }
   }
-  __device__ __forceinline__ void store(void* p) const {
+  __device__ __forceinline__ uint4 bits() const {
     if constexpr (BF16)
-      *static_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                           pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+      return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                        pack_bf16x2(f[6], f[7]));
     else
-      *static_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
 };
 
@@ -62,86 +61,113 @@ __device__ __forceinline__ void st1(void* p, int64_t e, float x) {
   }
 }
 
-// One head's work is cut into units.  Vector path (16-byte accesses, V
-// elements): half layout: rot/2/V units of a vector at m and one at m + rot/2,
-// interleaved: rot/V units of one vector; then (D - rot)/V copies.
-template <bool BF16>
-__device__ __forceinline__ int rope_units(int D, int pairs, bool inter) {
-  constexpr int V = Vec<BF16>::N;
-  return (inter ? 2 * pairs / V : pairs / V) + (D - 2 * pairs) / V;
+// One head's work is cut into units of 16-byte vectors of V elements.  Half
+// layout: pairs / V units of a vector at m and one at m + pairs; interleaved:
+// 2 pairs / V units of one vector; then (D - 2 pairs) / V copies.
+//
+// A thread takes one unit at a time: what counts is the number of threads in
+// flight (16384 rows of 40 heads of 128, bf16: 63 us; two units a thread at 48
+// registers 66, four at 78 registers 77).
+constexpr int kRopeBlocks = 6;   // resident blocks an SM: at most 40 registers
+
+// Place of pair m among a token's cosines and sines: a unit of G pairs reads
+// them two by two, and the same two of neighbouring units are neighbours, so
+// that the lanes of a warp read shared memory without conflicts.
+template <bool BF16, bool INTER>
+__device__ __forceinline__ int cs_place(int m, int pairs) {
+  constexpr int G = INTER ? Vec<BF16>::N / 2 : Vec<BF16>::N;
+  return ((m % G) / 2 * (pairs / G) + m / G) * 2 + m % 2;
 }
 
-// cs: the token's cosines and sines in shared memory (float2 per pair).
-template <bool BF16>
-__device__ __forceinline__ void rope_unit(const uint8_t* src, uint8_t* dst, int u, int pairs, bool inter,
-                                          const float2* cs, bool skip_copy) {
+struct Unit {
+  const uint8_t* src;
+  uint8_t* dst;
+  const float4* cs;     // of the unit's first two pairs; null: a copy
+};
+
+// Unit u of a head whose elements start at src / dst; cs: the token's cosines and sines.
+template <bool BF16, bool INTER>
+__device__ __forceinline__ Unit rope_unit(const uint8_t* src, uint8_t* dst, int u, int pairs, const float2* cs) {
+  const int nrot = (INTER ? 2 * pairs : pairs) / Vec<BF16>::N;
+  const bool rot = u < nrot;
+  const int o = (rot || INTER ? u : u + nrot) * 16;
+  return {src + o, dst + o, rot ? reinterpret_cast<const float4*>(cs) + u : nullptr};
+}
+
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void run_unit(const Unit& w, int pairs) {
   constexpr int V = Vec<BF16>::N;
-  constexpr int ES = BF16 ? 2 : 4;
-  const int nrot = inter ? 2 * pairs / V : pairs / V;
-  if (u >= nrot) {
-    if (skip_copy) return;
-    const int e = 2 * pairs + (u - nrot) * V;
-    *reinterpret_cast<uint4*>(dst + e * ES) = *reinterpret_cast<const uint4*>(src + e * ES);
+  const uint4 x = *reinterpret_cast<const uint4*>(w.src);
+  if (w.cs == nullptr) {
+    *reinterpret_cast<uint4*>(w.dst) = x;
     return;
   }
-  if (inter) {
-    Vec<BF16> a, y;
-    a.load(src + u * V * ES);
+  const int nu = pairs / (INTER ? V / 2 : V);
+  Vec<BF16> a(x);
+  if constexpr (INTER) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 c = w.cs[i / 4 * nu];
+      const float y = a.f[i] * c.x - a.f[i + 1] * c.y, z = a.f[i + 2] * c.z - a.f[i + 3] * c.w;
+      a.f[i + 1] = a.f[i + 1] * c.x + a.f[i] * c.y;
+      a.f[i + 3] = a.f[i + 3] * c.z + a.f[i + 2] * c.w;
+      a.f[i] = y;
+      a.f[i + 2] = z;
+    }
+  } else {
+    const int half = pairs * (BF16 ? 2 : 4);   // bytes from m to m + pairs
+    Vec<BF16> b(*reinterpret_cast<const uint4*>(w.src + half));
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
-      const float2 w = cs[u * (V / 2) + i / 2];
-      y.f[i] = a.f[i] * w.x - a.f[i + 1] * w.y;
-      y.f[i + 1] = a.f[i + 1] * w.x + a.f[i] * w.y;
+      const float4 c = w.cs[i / 2 * nu];
+      const float y = a.f[i] * c.x - b.f[i] * c.y, z = a.f[i + 1] * c.z - b.f[i + 1] * c.w;
+      b.f[i] = b.f[i] * c.x + a.f[i] * c.y;
+      b.f[i + 1] = b.f[i + 1] * c.z + a.f[i + 1] * c.w;
+      a.f[i] = y;
+      a.f[i + 1] = z;
     }
-    y.store(dst + u * V * ES);
-  } else {
-    Vec<BF16> a, b, ya, yb;
-    a.load(src + u * V * ES);
-    b.load(src + (pairs + u * V) * ES);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 w = cs[u * V + i];
-      ya.f[i] = a.f[i] * w.x - b.f[i] * w.y;
-      yb.f[i] = b.f[i] * w.x + a.f[i] * w.y;
-    }
-    ya.store(dst + u * V * ES);
-    yb.store(dst + (pairs + u * V) * ES);
+    *reinterpret_cast<uint4*>(w.dst + half) = b.bits();
   }
+  *reinterpret_cast<uint4*>(w.dst) = a.bits();
 }
 
 // Block: `tok` tokens of the chunk (their cosines and sines computed once in
 // shared memory, for all heads), threads over (token, head, unit).
-template <bool BF16>
-__global__ void __launch_bounds__(256) rope_fwd_kernel(const __grid_constant__ RopeArgs2 a,
+template <bool BF16, bool INTER>
+__global__ void __launch_bounds__(256, kRopeBlocks) rope_fwd_kernel(const __grid_constant__ RopeArgs2 a,
                                                        const __grid_constant__ RopeTable t, int tok) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float2 cs[];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
   const int nt = static_cast<int>(a.n_tokens - t0 < tok ? a.n_tokens - t0 : tok);
-  for (int i = threadIdx.x; i < nt * t.pairs; i += blockDim.x)
-    cs[i] = rope_cs(a.pos[t0 + i / t.pairs], t.turns[i % t.pairs], t.mscale);
+  for (int i = threadIdx.x; i < nt * t.pairs; i += blockDim.x) {
+    const int r = i / t.pairs, m = i - r * t.pairs;
+    cs[a.vec ? r * t.pairs + cs_place<BF16, INTER>(m, t.pairs) : i] = rope_cs(a.pos[t0 + r], t.turns[m], t.mscale);
+  }
   __syncthreads();
   constexpr int ES = BF16 ? 2 : 4;
-  const bool inter = t.interleaved != 0;
+  const int items = nt * a.n_heads * static_cast<int>(a.units.d);
   if (a.vec) {
-    const int units = rope_units<BF16>(a.head_dim, t.pairs, inter);
-    for (int i = threadIdx.x; i < nt * a.n_heads * units; i += blockDim.x) {
-      const int u = i % units, h = (i / units) % a.n_heads, r = i / (units * a.n_heads);
-      const uint8_t* src = static_cast<const uint8_t*>(a.x.p) + ((t0 + r) * a.x.row + h * a.x.head) * ES;
-      uint8_t* dst = static_cast<uint8_t*>(a.y) + ((t0 + r) * a.y_row + h * a.y_head) * ES;
-      rope_unit<BF16>(src, dst, u, t.pairs, inter, cs + r * t.pairs, a.in_place);
+    for (int i = threadIdx.x; i < items; i += 256) {
+      const int rh = a.units.div(i), u = i - rh * static_cast<int>(a.units.d);
+      const int r = a.heads.div(rh), h = rh - r * a.n_heads;
+      const Unit w = rope_unit<BF16, INTER>(
+          static_cast<const uint8_t*>(a.x.p) + ((t0 + r) * a.x.row + h * a.x.head) * ES,
+          static_cast<uint8_t*>(a.y) + ((t0 + r) * a.y_row + h * a.y_head) * ES, u, t.pairs, cs + r * t.pairs);
+      if (w.cs == nullptr && a.in_place) continue;
+      run_unit<BF16, INTER>(w, t.pairs);
     }
   } else {   // element by element: unit = one pair, or one copied element
-    const int units = t.pairs + a.head_dim - 2 * t.pairs;
-    for (int i = threadIdx.x; i < nt * a.n_heads * units; i += blockDim.x) {
-      const int u = i % units, h = (i / units) % a.n_heads, r = i / (units * a.n_heads);
+    for (int i = threadIdx.x; i < items; i += blockDim.x) {
+      const int rh = a.units.div(i), u = i - rh * static_cast<int>(a.units.d);
+      const int r = a.heads.div(rh), h = rh - r * a.n_heads;
       const int64_t xs = (t0 + r) * a.x.row + h * a.x.head, ys = (t0 + r) * a.y_row + h * a.y_head;
       if (u >= t.pairs) {
         if (!a.in_place) st1<BF16>(a.y, ys + t.pairs + u, ld1<BF16>(a.x.p, xs + t.pairs + u));
         continue;
       }
-      const int e0 = inter ? 2 * u : u, e1 = inter ? 2 * u + 1 : u + t.pairs;
+      const int e0 = INTER ? 2 * u : u, e1 = INTER ? 2 * u + 1 : u + t.pairs;
       const float2 w = cs[r * t.pairs + u];
       const float x0 = ld1<BF16>(a.x.p, xs + e0), x1 = ld1<BF16>(a.x.p, xs + e1);
       st1<BF16>(a.y, ys + e0, x0 * w.x - x1 * w.y);
@@ -153,23 +179,26 @@ __global__ void __launch_bounds__(256) rope_fwd_kernel(const __grid_constant__ R
 // Grid (row blocks of a sequence, sequences).  Threads over (token, head,
 // unit) with the heads numbered q, k, v; v (and all of them without rope) is
 // copied in 16-byte units.
-template <bool BF16>
-__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ AppendArgs a,
+template <bool BF16, bool INTER>
+__global__ void __launch_bounds__(256, kRopeBlocks) paged_append_kernel(const __grid_constant__ AppendArgs a,
                                                            const __grid_constant__ RopeTable t, int tok) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float2 cs[];
-  __shared__ int64_t s_row[32];   // row of K/V head 0, or -1 (tok <= 32)
+  extern __shared__ __align__(16) float2 cs[];
+  __shared__ int64_t s_row[kMaxTok];   // row of K/V head 0, or -1
   const int s = blockIdx.y;
   const SeqSpan sp = seq_span(a.c, a.ch, s);
   const int t0 = blockIdx.x * tok;
   const int nt = min(sp.n - t0, tok);
   if (nt <= 0) return;
   if (sp.over && threadIdx.x == 0) report_bad_cache(a.status, s);
-  const int64_t pos0 = a.rope ? a.pos[s] + t0 : 0;
-  if (a.rope)
-    for (int i = threadIdx.x; i < nt * t.pairs; i += blockDim.x)
-      cs[i] = rope_cs(pos0 + i / t.pairs, t.turns[i % t.pairs], t.mscale);
+  if (t.pairs > 0) {
+    const int64_t pos0 = a.pos[s] + t0;
+    for (int i = threadIdx.x; i < nt * t.pairs; i += blockDim.x) {
+      const int r = i / t.pairs, m = i - r * t.pairs;
+      cs[r * t.pairs + cs_place<BF16, INTER>(m, t.pairs)] = rope_cs(pos0 + r, t.turns[m], t.mscale);
+    }
+  }
   if (threadIdx.x < nt) {
     const int j = sp.old + t0 + static_cast<int>(threadIdx.x);
     const int64_t row = j < sp.kv ? slot_row(a.c, s, 0, j) : -1;
@@ -178,40 +207,37 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
   }
   __syncthreads();
   constexpr int ES = BF16 ? 2 : 4;
-  const int D = a.head_dim, V = 16 / ES, ps = a.c.page.d;
-  const bool inter = t.interleaved != 0;
-  const int Hk = a.c.n_heads, Hq = a.n_q_heads;
+  const int row_bytes = a.head_dim * ES, cu = row_bytes / 16, ps = a.c.page.d;
+  const int Hk = a.c.n_heads, Hq = a.n_q_heads, ru = a.units.d;
   const int64_t g0 = sp.row0 + t0;
-  const int ru = a.rope ? rope_units<BF16>(D, t.pairs, inter) : D / V, cu = D / V;
-  const int nrot = (Hq + Hk) * ru, per = nrot + Hk * cu;
-  for (int i = threadIdx.x; i < nt * per; i += blockDim.x) {
-    const int r = i / per, w = i - r * per;
-    if (w < nrot) {
-      const int h = w / ru, u = w - h * ru;
-      const uint8_t* src;
-      uint8_t* dst;
-      bool same = false;
+  const int nrot = (Hq + Hk) * ru, items = nt * static_cast<int>(a.per.d);
+  for (int i = threadIdx.x; i < items; i += 256) {
+    const int r = a.per.div(i), x = i - r * static_cast<int>(a.per.d);
+    const int64_t to = s_row[r];
+    const float2* c = cs + r * t.pairs;
+    Unit w;
+    if (x < nrot) {
+      const int h = a.units.div(x), u = x - h * ru;
       if (h < Hq) {
-        src = static_cast<const uint8_t*>(a.q.p) + ((g0 + r) * a.q.row + h * a.q.head) * ES;
-        dst = static_cast<uint8_t*>(a.q_out) + ((g0 + r) * a.qo_row + h * a.qo_head) * ES;
-        same = src == dst;
+        w = rope_unit<BF16, INTER>(static_cast<const uint8_t*>(a.q.p) + ((g0 + r) * a.q.row + h * a.q.head) * ES,
+                                   static_cast<uint8_t*>(a.q_out) + ((g0 + r) * a.qo_row + h * a.qo_head) * ES, u,
+                                   t.pairs, c);
+        if (w.cs == nullptr && w.src == w.dst) continue;   // in place
       } else {
-        if (s_row[r] < 0) continue;
-        src = static_cast<const uint8_t*>(a.k.p) + ((g0 + r) * a.k.row + (h - Hq) * a.k.head) * ES;
-        dst = static_cast<uint8_t*>(a.k_pool) + (s_row[r] + static_cast<int64_t>(h - Hq) * ps) * D * ES;
+        if (to < 0) continue;
+        w = rope_unit<BF16, INTER>(static_cast<const uint8_t*>(a.k.p) + ((g0 + r) * a.k.row + (h - Hq) * a.k.head) * ES,
+                                   static_cast<uint8_t*>(a.k_pool) + (to + static_cast<int64_t>(h - Hq) * ps) * row_bytes,
+                                   u, t.pairs, c);
       }
-      if (a.rope)
-        rope_unit<BF16>(src, dst, u, t.pairs, inter, cs + r * t.pairs, same);
-      else
-        *reinterpret_cast<uint4*>(dst + u * 16) = *reinterpret_cast<const uint4*>(src + u * 16);
-    } else if (s_row[r] >= 0) {
-      const int h = (w - nrot) / cu, u = (w - nrot) - h * cu;
-      const int64_t row = s_row[r] + static_cast<int64_t>(h) * ps;
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.v_pool) + row * D * ES + u * 16) =
-          *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.v.p) +
-                                          ((g0 + r) * a.v.row + h * a.v.head) * ES + u * 16);
+    } else {
+      if (to < 0) continue;
+      const int h = (x - nrot) / cu, u = (x - nrot) - h * cu;
+      const int64_t row = to + static_cast<int64_t>(h) * ps;
+      w = {static_cast<const uint8_t*>(a.v.p) + ((g0 + r) * a.v.row + h * a.v.head) * ES + u * 16,
+           static_cast<uint8_t*>(a.v_pool) + row * row_bytes + u * 16, nullptr};
       if (a.acc != nullptr && u == 0) a.acc[row] = 0.f;
     }
+    run_unit<BF16, INTER>(w, t.pairs);
   }
 }
 
@@ -242,17 +268,21 @@ __device__ __forceinline__ int64_t evict_len(const EvictArgs& a, int s, bool* ba
   return len < 0 ? 0 : len < cap ? len : cap;
 }
 
-constexpr int kSelThreads = 1024;
-
 // CTA per (head, sequence, layer): the bar (the (m - r)-th largest key among
-// the first L - r slots) by a radix selection of four 8-bit digits, then one
-// pass that writes the kept slots in slot order, counting equals of the bar
-// from the lowest slot.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
+// the first n = L - r slots) by a radix selection of 8-bit digits, from keys
+// read once into shared memory (when they fit), then the kept slots in slot
+// order, with the bar's equals taken from the lowest slot.  The histogram has
+// kSelCopies copies, one per lane modulo kSelCopies, because weights crowd
+// into few bins; the selection stops as soon as a whole bin is wanted.
+constexpr int kSelCopies = 8;
+
+template <int T>
+__global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__ EvictArgs a, int max_keys) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int hist[256];
-  __shared__ int s_digit, s_rest;
+  extern __shared__ uint32_t keys[];                 // max_keys
+  __shared__ int hist[kSelCopies][257];
+  __shared__ int s_digit, s_rest, s_whole;
   __shared__ int wsum[2][32];
   const int h = blockIdx.x, s = blockIdx.y, l = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -263,178 +293,217 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   const int r = static_cast<int>(a.recent < m ? a.recent : m);
   const int n = L - r, want = m - r;
   int32_t* out = a.kept + ((static_cast<int64_t>(l) * a.src.n_seqs + s) * a.src.n_heads + h) * a.kept_stride;
-  const float* acc = a.acc + l * a.src_layer_rows;
-  for (int i = tid; i < r; i += kSelThreads) out[want + i] = n + i;
+  for (int i = tid; i < r; i += T) out[want + i] = n + i;
+  if (want == n) {   // none has to go
+    for (int i = tid; i < n; i += T) out[i] = i;
+    return;
+  }
   if (want <= 0) return;
-  auto key_at = [&](int j) -> uint32_t {
+  const float* acc = a.acc + l * a.src_layer_rows;
+  const bool fits = n <= max_keys;
+  auto from_pool = [&](int j) -> uint32_t {
     const int64_t row = slot_row(a.src, s, h, j);
     return row < 0 ? 0u : weight_key(acc[row]);
   };
+  if (fits) {
+#pragma unroll 4
+    for (int j = tid; j < n; j += T) keys[j] = from_pool(j);
+  }
+  auto key_at = [&](int j) { return fits ? keys[j] : from_pool(j); };
   uint32_t bar = 0, mask = 0;
   int rest = want;   // how many of the keys that match bar's known digits are wanted
-  if (want < n) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int j = tid; j < n; j += kSelThreads) {
-        const uint32_t key = key_at(j);
-        if ((key & mask) == bar) atomicAdd(&hist[(key >> shift) & 255u], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int left = rest, d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        s_digit = d;
-        s_rest = left;
-      }
-      __syncthreads();
-      bar |= static_cast<uint32_t>(s_digit) << shift;
-      mask |= 255u << shift;
-      rest = s_rest;
-      __syncthreads();
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < kSelCopies * 257; i += T) hist[0][i] = 0;
+    __syncthreads();   // also: the keys are there
+    for (int j = tid; j < n; j += T) {
+      const uint32_t key = key_at(j);
+      if ((key & mask) == bar) atomicAdd(&hist[lane % kSelCopies][(key >> shift) & 255u], 1);
     }
+    __syncthreads();
+    // Counts of the bins above: a suffix sum over the 256 bins, in 8 warps.
+    int c = 0, incl = 0;
+    if (tid < 256) {
+#pragma unroll
+      for (int k = 0; k < kSelCopies; ++k) c += hist[k][tid];
+      incl = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, incl, off);
+        if (lane + off < 32) incl += y;
+      }
+      if (lane == 0) wsum[0][warp] = incl;
+    }
+    __syncthreads();
+    if (tid < 256) {
+      for (int w = warp + 1; w < 8; ++w) incl += wsum[0][w];
+      if (incl >= rest && incl - c < rest) {
+        s_digit = tid;
+        s_rest = rest - (incl - c);
+        s_whole = s_rest == c;
+      }
+    }
+    __syncthreads();
+    bar |= static_cast<uint32_t>(s_digit) << shift;
+    mask |= 255u << shift;
+    rest = s_rest;
+    if (s_whole) break;
   }
-  // Keys above the bar are kept, and the first `rest` of its equals (all of
-  // the slots when none has to go).
-  int kept = 0, equals = 0;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    bool more = false, same = false;
-    if (j < n) {
-      if (want == n) {
-        more = true;
-      } else {
-        const uint32_t key = key_at(j);
-        more = key > bar;
-        same = key == bar;
-      }
-    }
-    const uint32_t bs = __ballot_sync(0xffffffffu, same);
-    if (lane == 0) wsum[0][warp] = __popc(bs);
-    __syncthreads();
-    int before = equals, total = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += wsum[0][w];
-      total += wsum[0][w];
-    }
-    const bool take = more || (same && before + __popc(bs & ((1u << lane) - 1)) < rest);
+  // Keys above the bar are kept, and the first `rest` of its equals (in the
+  // digits looked at).  Each warp owns a run of slots: it counts them, then
+  // writes them behind those of the warps before it.
+  const int run = (n + T - 1) / T * 32, j0 = min(warp * run, n), j1 = min(j0 + run, n);
+  int more = 0, same = 0;
+  for (int j = j0 + lane; j < j1; j += 32) {
+    const uint32_t key = key_at(j) & mask;
+    more += key > bar;
+    same += key == bar;
+  }
+  more = __reduce_add_sync(0xffffffffu, more);
+  same = __reduce_add_sync(0xffffffffu, same);
+  __syncthreads();
+  if (lane == 0) {
+    wsum[0][warp] = more;
+    wsum[1][warp] = same;
+  }
+  __syncthreads();
+  more = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[0][lane] : 0);
+  same = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[1][lane] : 0);   // equals before this warp
+  int at = more + min(same, rest);
+  for (int j = j0; j < j1; j += 32) {
+    const uint32_t key = j + lane < j1 ? key_at(j + lane) & mask : 0u;
+    const bool eq = j + lane < j1 && key == bar;
+    const uint32_t be = __ballot_sync(0xffffffffu, eq);
+    const uint32_t below = (1u << lane) - 1u;
+    const bool take = j + lane < j1 && (key > bar || (eq && same + __popc(be & below) < rest));
     const uint32_t bt = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) wsum[1][warp] = __popc(bt);
-    __syncthreads();
-    int at = kept, taken = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) at += wsum[1][w];
-      taken += wsum[1][w];
-    }
-    if (take) out[at + __popc(bt & ((1u << lane) - 1))] = j;
-    equals += total;
-    kept += taken;
-    __syncthreads();
+    if (take) out[at + __popc(bt & below)] = j + lane;
+    at += __popc(bt);
+    same += __popc(be);
   }
 }
 
-// Grid (head x slice, sequence, layer).  The kept rows move to the front in
-// slot order.  In place a row's new slot is never above its old one, so a CTA
-// that reads a chunk of rows before it writes that chunk, chunk after chunk,
-// never overwrites a row it still has to read; the K and V rows are cut into
-// slices of 64 bytes that different CTAs move, each for itself.
+// The kept rows move to the front in slot order: CTA per (layer, head, slice,
+// block of rows, sequence).  The K and V rows of a slot are one row of 2 *
+// row_bytes / 16 chunks, cut into `slices`; a block holds kMoveChunks chunks,
+// so that a thread has kMoveDeep 16-byte loads in flight.  To pages of its own
+// every block is a CTA.  In place a row's new slot is never above its old one,
+// so a CTA that walks all blocks in order, reading a block before it writes it,
+// never overwrites a row it still has to read (slices are independent).
 constexpr int kMoveThreads = 256;
-constexpr int kSliceBytes = 64;                              // of a K or V row
-constexpr int kMoveRows = kMoveThreads / (kSliceBytes / 16); // rows of a chunk: 64
-constexpr int kMoveDeep = 4;                                 // chunks read together
+constexpr int kMoveDeep = 4;
+constexpr int kMoveChunks = kMoveThreads * kMoveDeep;
+constexpr int kMoveMaxRows = 256;   // of a block: slices of at least 4 chunks
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int slices) {
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int slices,
+                                                                  int blocks) {
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.x / slices, slice = blockIdx.x % slices, s = blockIdx.y, l = blockIdx.z;
+  __shared__ int64_t s_from[kMoveMaxRows], s_to[kMoveMaxRows];
+  int id = blockIdx.x;
+  const int blk = id % blocks;
+  id /= blocks;
+  const int slice = id % slices;
+  id /= slices;
+  const int h = id % a.src.n_heads, l = id / a.src.n_heads, s = blockIdx.y;
+  const int tid = threadIdx.x;
+  const bool in_place = a.k == a.dk;
+  // In place another CTA may have stored the new length m already: min(keep, m) is m again.
+  const int64_t dcap = static_cast<int64_t>(a.dst.max_pages) * a.dst.page.d;
   bool bad;
   const int64_t L = evict_len(a, s, &bad);
   const int m = static_cast<int>(a.keep < L ? a.keep : L);
-  const int64_t dcap = static_cast<int64_t>(a.dst.max_pages) * a.dst.page.d;
+  const int all = 2 * a.row_bytes / 16, cols = all / slices, rows = kMoveChunks / cols;
   const int32_t* kept = a.kept + ((static_cast<int64_t>(l) * a.src.n_seqs + s) * a.src.n_heads + h) * a.kept_stride;
-  const bool in_place = a.k == a.dk;
-  const int per_tensor = (slices - 1) / 2;   // slices of K, then of V, then one of acc
-  auto rows_of = [&](int i, int64_t* from, int64_t* to) {
-    *from = slot_row(a.src, s, h, kept[i]);
-    *to = i < dcap ? slot_row(a.dst, s, h, i) : -1;
-    if (*from < 0 || *to < 0) report_bad_cache(a.status, s);
-  };
-  if (slice == slices - 1) {
-    const float* src = a.acc + l * a.src_layer_rows;
-    float* dst = a.dacc + l * a.dst_layer_rows;
-    for (int i0 = 0; i0 < m; i0 += kMoveThreads) {
-      const int i = i0 + threadIdx.x;
-      int64_t from = -1, to = -1;
-      if (i < m) rows_of(i, &from, &to);
-      const float x = from >= 0 ? src[from] : 0.f;
-      if (in_place) __syncthreads();
-      if (to >= 0 && !(in_place && from == to)) dst[to] = x;
+  for (int i0 = blk * rows; i0 < m; i0 += blocks * rows) {
+    const int nr = min(rows, m - i0);
+    float w = 0.f;
+    int64_t from = -1, to = -1;
+    if (tid < nr) {
+      const int i = i0 + tid;
+      from = slot_row(a.src, s, h, kept[i]);
+      to = i < dcap ? slot_row(a.dst, s, h, i) : -1;
+      if (from < 0 || to < 0) report_bad_cache(a.status, s);
+      if (in_place && from == to) to = -1;
+      if (slice == 0 && from >= 0 && to >= 0) w = a.acc[l * a.src_layer_rows + from];
+      s_from[tid] = from;
+      s_to[tid] = to;
     }
-    return;
-  }
-  const bool is_v = slice >= per_tensor;
-  const int64_t byte0 = static_cast<int64_t>(is_v ? slice - per_tensor : slice) * kSliceBytes +
-                        (threadIdx.x % (kSliceBytes / 16)) * 16;
-  const uint8_t* src = (is_v ? a.v : a.k) + l * a.src_layer_rows * a.row_bytes + byte0;
-  uint8_t* dst = (is_v ? a.dv : a.dk) + l * a.dst_layer_rows * a.row_bytes + byte0;
-  const int rr = threadIdx.x / (kSliceBytes / 16);
-  for (int i0 = 0; i0 < m; i0 += kMoveRows * kMoveDeep) {
+    __syncthreads();
     uint4 x[kMoveDeep];
-    int64_t from[kMoveDeep], to[kMoveDeep];
 #pragma unroll
     for (int d = 0; d < kMoveDeep; ++d) {
-      const int i = i0 + d * kMoveRows + rr;
-      from[d] = to[d] = -1;
+      const int e = d * kMoveThreads + tid, r = e / cols, c = slice * cols + e % cols;
       x[d] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < m) rows_of(i, &from[d], &to[d]);
-      if (from[d] >= 0 && !(in_place && from[d] == to[d])) x[d] = *reinterpret_cast<const uint4*>(src + from[d] * a.row_bytes);
+      if (r >= nr || s_to[r] < 0 || s_from[r] < 0) continue;
+      const bool is_v = c >= all / 2;
+      x[d] = *reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + (l * a.src_layer_rows + s_from[r]) * a.row_bytes +
+                                             (is_v ? c - all / 2 : c) * 16);
     }
     if (in_place) __syncthreads();
+    if (slice == 0 && to >= 0) a.dacc[l * a.dst_layer_rows + to] = w;
 #pragma unroll
-    for (int d = 0; d < kMoveDeep; ++d)
-      if (to[d] >= 0 && !(in_place && from[d] == to[d])) *reinterpret_cast<uint4*>(dst + to[d] * a.row_bytes) = x[d];
+    for (int d = 0; d < kMoveDeep; ++d) {
+      const int e = d * kMoveThreads + tid, r = e / cols, c = slice * cols + e % cols;
+      if (r >= nr || s_to[r] < 0) continue;
+      const bool is_v = c >= all / 2;
+      *reinterpret_cast<uint4*>((is_v ? a.dv : a.dk) + (l * a.dst_layer_rows + s_to[r]) * a.row_bytes +
+                                (is_v ? c - all / 2 : c) * 16) = x[d];
+    }
+    __syncthreads();   // s_from and s_to are rewritten
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    if (a.dst_pos != a.src_pos) a.dst_pos[s] = a.src_pos[s];
+    a.dst_lens[s] = m < dcap ? m : dcap;
   }
 }
 
-__global__ void evict_lens_kernel(const __grid_constant__ EvictArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int s = blockIdx.x * blockDim.x + threadIdx.x;
-  if (s >= a.src.n_seqs) return;
-  bool bad;
-  const int64_t L = evict_len(a, s, &bad);
-  const int64_t dcap = static_cast<int64_t>(a.dst.max_pages) * a.dst.page.d;
-  const int64_t m = a.keep < L ? a.keep : L;
-  a.dst_lens[s] = m < dcap ? m : dcap;
-  if (a.dst_pos != a.src_pos) a.dst_pos[s] = a.src_pos[s];
+template <bool BF16>
+cudaError_t launch_rope_t(cudaStream_t stream, const RopeArgs2& a, const RopeTable& t, int tok) {
+  const dim3 grid(static_cast<unsigned>((a.n_tokens + tok - 1) / tok));
+  const size_t smem = static_cast<size_t>(tok) * t.pairs * sizeof(float2);
+  return t.interleaved ? launch_kernel(rope_fwd_kernel<BF16, true>, grid, dim3(256), smem, stream, a, t, tok)
+                       : launch_kernel(rope_fwd_kernel<BF16, false>, grid, dim3(256), smem, stream, a, t, tok);
+}
+
+template <bool BF16>
+cudaError_t launch_append_t(cudaStream_t stream, const AppendArgs& a, const RopeTable& t, int tok) {
+  const dim3 grid(static_cast<unsigned>((a.ch.max_q + tok - 1) / tok), static_cast<unsigned>(a.c.n_seqs));
+  const size_t smem = static_cast<size_t>(tok) * t.pairs * sizeof(float2);
+  return t.interleaved ? launch_kernel(paged_append_kernel<BF16, true>, grid, dim3(256), smem, stream, a, t, tok)
+                       : launch_kernel(paged_append_kernel<BF16, false>, grid, dim3(256), smem, stream, a, t, tok);
+}
+
+// Tokens per block: about 32 KB of rows, to spread the angles and the page
+// lookups over (16 KB: append of 12000 rows 3% slower, 64 KB as well); one
+// token when that would leave SMs without a block.
+int tokens_per_block(int64_t row_bytes, int64_t tokens) {
+  int64_t tok = (32768 + row_bytes - 1) / row_bytes;
+  tok = tok < 1 ? 1 : tok > kMaxTok ? kMaxTok : tok;
+  return tokens < tok * 148 ? 1 : static_cast<int>(tok);
 }
 
 }  // namespace
 
-cudaError_t launch_rope_rows(cudaStream_t stream, const RopeArgs2& a, const RopeTable& t) {
-  // Tokens per block: about 16 KB of rows, so that few heads do not leave
-  // blocks of a handful of threads' work, at most 32 tokens.
-  const int64_t row = static_cast<int64_t>(a.n_heads) * a.head_dim * (a.bf16 ? 2 : 4);
-  int64_t tok = (16384 + row - 1) / row;
-  tok = tok < 1 ? 1 : tok > 32 ? 32 : tok;
-  if (a.n_tokens < tok * 148) tok = 1;
-  const unsigned grid = static_cast<unsigned>((a.n_tokens + tok - 1) / tok);
-  const size_t smem = static_cast<size_t>(tok) * t.pairs * sizeof(float2);
-  return a.bf16 ? launch_kernel(rope_fwd_kernel<true>, dim3(grid), dim3(256), smem, stream, a, t, static_cast<int>(tok))
-                : launch_kernel(rope_fwd_kernel<false>, dim3(grid), dim3(256), smem, stream, a, t,
-                                static_cast<int>(tok));
+cudaError_t launch_rope_rows(cudaStream_t stream, const RopeArgs2& in, const RopeTable& t) {
+  RopeArgs2 a = in;
+  const int es = a.bf16 ? 2 : 4;
+  const int v = 16 / es, pairs = t.pairs, D = a.head_dim;
+  a.heads = FastDiv::make(static_cast<uint32_t>(a.n_heads));
+  a.units = FastDiv::make(static_cast<uint32_t>(a.vec ? (t.interleaved ? D : D - pairs) / v : D - pairs));
+  const int tok = tokens_per_block(static_cast<int64_t>(a.n_heads) * D * es, a.n_tokens);
+  return a.bf16 ? launch_rope_t<true>(stream, a, t, tok) : launch_rope_t<false>(stream, a, t, tok);
 }
 
-cudaError_t launch_paged_append(cudaStream_t stream, const AppendArgs& a, const RopeTable& t) {
-  const int64_t row = static_cast<int64_t>(a.n_q_heads + 2 * a.c.n_heads) * a.head_dim * (a.bf16 ? 2 : 4);
-  int64_t tok = (16384 + row - 1) / row;
-  tok = tok < 1 ? 1 : tok > 32 ? 32 : tok;
-  if (static_cast<int64_t>(a.ch.max_q) * a.c.n_seqs < tok * 148) tok = 1;
-  const dim3 grid(static_cast<unsigned>((a.ch.max_q + tok - 1) / tok), static_cast<unsigned>(a.c.n_seqs));
-  const size_t smem = a.rope ? static_cast<size_t>(tok) * t.pairs * sizeof(float2) : 0;
-  return a.bf16 ? launch_kernel(paged_append_kernel<true>, grid, dim3(256), smem, stream, a, t, static_cast<int>(tok))
-                : launch_kernel(paged_append_kernel<false>, grid, dim3(256), smem, stream, a, t,
-                                static_cast<int>(tok));
+cudaError_t launch_paged_append(cudaStream_t stream, const AppendArgs& in, const RopeTable& t) {
+  AppendArgs a = in;
+  const int es = a.bf16 ? 2 : 4;
+  const int v = 16 / es, D = a.head_dim;
+  const int ru = (t.interleaved ? D : D - t.pairs) / v;
+  a.units = FastDiv::make(static_cast<uint32_t>(ru));
+  a.per = FastDiv::make(static_cast<uint32_t>((a.n_q_heads + a.c.n_heads) * ru + a.c.n_heads * (D / v)));
+  const int tok = tokens_per_block(static_cast<int64_t>(a.n_q_heads + 2 * a.c.n_heads) * D * es,
+                                   static_cast<int64_t>(a.ch.max_q) * a.c.n_seqs);
+  return a.bf16 ? launch_append_t<true>(stream, a, t, tok) : launch_append_t<false>(stream, a, t, tok);
 }
 
 cudaError_t launch_paged_advance(cudaStream_t stream, const PagedView& c, const ChunkArgs& ch, int64_t* lens,
@@ -444,14 +513,35 @@ cudaError_t launch_paged_advance(cudaStream_t stream, const PagedView& c, const 
 }
 
 cudaError_t launch_paged_evict(const Launch& L, const EvictArgs& a) {
-  const unsigned S = static_cast<unsigned>(a.src.n_seqs), nl = static_cast<unsigned>(a.n_layers);
-  const unsigned H = static_cast<unsigned>(a.src.n_heads);
-  cudaError_t e = launch_kernel(evict_select_kernel, dim3(H, S, nl), dim3(kSelThreads), 0, L.stream, a);
+  const int64_t S = a.src.n_seqs, H = a.src.n_heads, nl = a.n_layers;
+  // Keys in shared memory: all that the tables can hold, up to 48 K.  Few keys
+  // get small CTAs, of which several share an SM.
+  const int64_t cap = static_cast<int64_t>(a.src.max_pages) * a.src.page.d;
+  const int max_keys = static_cast<int>(cap < 49152 ? cap : 49152);
+  const dim3 sel(static_cast<unsigned>(H), static_cast<unsigned>(S), static_cast<unsigned>(nl));
+  // launch_kernel raises a kernel's limit from 48 KB of dynamic shared memory on; the static arrays need room below it.
+  size_t smem = static_cast<size_t>(max_keys) * 4;
+  if (smem > 36 * 1024 && smem <= 48 * 1024) smem = 48 * 1024 + 16;
+  cudaError_t e = cap <= 4096
+                      ? launch_kernel(evict_select_kernel<256>, sel, dim3(256), smem, L.stream, a, max_keys)
+                      : launch_kernel(evict_select_kernel<1024>, sel, dim3(1024), smem, L.stream, a, max_keys);
   if (e != cudaSuccess) return e;
-  const int slices = 2 * (a.row_bytes / kSliceBytes) + 1;
-  e = launch_kernel(evict_move_kernel, dim3(H * slices, S, nl), dim3(kMoveThreads), 0, L.stream, a, slices);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(evict_lens_kernel, dim3((S + 127) / 128), dim3(128), 0, L.stream, a);
+  // To other pages: whole rows, every block a CTA.  In place: one CTA walks a
+  // slice's blocks, so slices (of at least 64 bytes) are cut until there are
+  // about four CTAs for each SM.
+  const int all = 2 * a.row_bytes / 16;
+  int slices = 1;
+  int64_t blocks = 1;
+  if (a.k == a.dk) {
+    while (all / slices > 4 && nl * H * S * slices < 4 * L.sm_count) slices *= 2;
+  } else {
+    const int rows = kMoveChunks / all;
+    blocks = (a.keep + rows - 1) / rows;
+    const int64_t most = (1ll << 30) / (nl * H);   // the grid's x dimension
+    blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
+  }
+  return launch_kernel(evict_move_kernel, dim3(static_cast<unsigned>(nl * H * slices * blocks), static_cast<unsigned>(S)),
+                       dim3(kMoveThreads), 0, L.stream, a, slices, static_cast<int>(blocks));
 }
 
 }  // namespace vx

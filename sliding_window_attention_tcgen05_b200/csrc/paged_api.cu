@@ -129,8 +129,14 @@ vx_status rope_table(const vx_rope_cfg* r, int head_dim, RopeTable* t, const cha
   if (r->scaling == VX_ROPE_NTK) theta *= powl(r->factor, static_cast<long double>(rot) / (rot - 2));
   const long double two_pi = 6.283185307179586476925286766559L;
   for (int m = 0; m < kMaxRotPairs; ++m) t->turns[m] = 0;
+  // theta^(-2m / rot) as the product over m's bits: a power for each bit, one
+  // multiplication for each m (64 powl calls take longer than the launch).
+  long double bit[7], pw[kMaxRotPairs];
+  for (int b = 0; b < 7; ++b) bit[b] = powl(theta, -2.0L * (1 << b) / rot);
+  pw[0] = 1.0L;
   for (int m = 0; m < rot / 2; ++m) {
-    long double f = powl(theta, -2.0L * m / rot);
+    if (m > 0) pw[m] = pw[m & (m - 1)] * bit[__builtin_ctz(m)];
+    long double f = pw[m];
     if (r->scaling == VX_ROPE_LINEAR) f /= r->factor;
     if (yarn) {
       long double g = (r->orig_len * f / two_pi - r->beta_slow) /
@@ -264,7 +270,6 @@ vx_status vx_paged_append(const vx_paged_cache* cache, int layer, const vx_rope_
   a.v = {v->p, v->row, v->head};
   a.head_dim = cache->head_dim;
   a.bf16 = cache->dt == VX_BF16;
-  a.rope = rope != nullptr;
   a.status = L.status;
   VX_CUDA(traced(L, "paged_append", 1, [&] { return launch_paged_append(stream, a, t); }));
   return VX_OK;
@@ -430,7 +435,7 @@ vx_status vx_paged_evict(const vx_paged_cache* cache, const vx_paged_cache* dst,
   a.kept_stride = keep < cap || kept == nullptr ? a.keep : keep;
   a.kept = kept ? kept : reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kAlign);
   a.status = L.status;
-  VX_CUDA(traced(L, "paged_evict", 3, [&] { return launch_paged_evict(L, a); }));
+  VX_CUDA(traced(L, "paged_evict", 2, [&] { return launch_paged_evict(L, a); }));
   return VX_OK;
 }
 

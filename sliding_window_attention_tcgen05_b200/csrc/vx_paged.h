@@ -77,10 +77,11 @@ __device__ __forceinline__ int64_t slot_row(const PagedView& c, int s, int head,
 // pos * turns[m] mod 2^64 is the fraction of a turn of pos * f_m exactly up to
 // |pos| * 2^-65 turns, for any 64-bit position.
 constexpr int kMaxRotPairs = 128;
+constexpr int kMaxTok = 32;   // tokens of a block
 struct RopeTable {
   uint64_t turns[kMaxRotPairs];
   float mscale;
-  int pairs;           // rot_dim / 2
+  int pairs;           // rot_dim / 2 (0: copies only)
   int interleaved;
 };
 
@@ -98,6 +99,7 @@ struct RopeArgs2 {
   int64_t n_tokens;
   int n_heads, head_dim;
   bool bf16, vec, in_place;   // vec: 16-byte accesses of 8 (bf16) or 4 (fp32) elements are possible
+  FastDiv units, heads;       // work units of a head, heads (set by the launcher)
 };
 cudaError_t launch_rope_rows(cudaStream_t stream, const RopeArgs2& a, const RopeTable& t);
 
@@ -111,7 +113,8 @@ struct AppendArgs {
   void* q_out;
   int64_t qo_row, qo_head;
   int n_q_heads, head_dim;
-  bool bf16, rope;
+  bool bf16;
+  FastDiv units, per;      // work units of a rotated head, of a token (set by the launcher)
   DevStatus* status;
 };
 cudaError_t launch_paged_append(cudaStream_t stream, const AppendArgs& a, const RopeTable& t);

@@ -478,7 +478,8 @@ def test_attention_refusals():
     ([100, 33], 2, 128, 7, 30, 50, "rand"), ([1500, 3000, 700], 3, 64, 50, 999, 1, "ties"),
     ([5000, 1025, 1024], 1, 64, 64, 1024, 0, "ties"), ([40, 70], 2, 64, 16, 20, 5, "odd"),
     ([40, 70], 2, 64, 16, 0, 5, "rand"), ([40, 70], 2, 64, 16, 1000, 5, "rand"),
-    ([2600, 2100], 2, 64, 33, 2050, 7, "zero")])
+    ([2600, 2100], 2, 64, 33, 2050, 7, "zero"), ([11000, 9000], 1, 64, 128, 3001, 64, "rand"),
+    ([60000], 1, 64, 512, 20000, 100, "ties")])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_evict(dtype, lens, hkv, D, page, keep, recent, kind, in_place):
     vx = _vx()

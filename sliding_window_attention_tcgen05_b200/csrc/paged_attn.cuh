@@ -4,8 +4,12 @@
 //
 // A block of queries (tokens t_first .. t_last of one sequence) sees the slots
 // [0, pre) and [lo, hi).  They are walked as one list x = 0 .. total - 1: slot
-// j = x for x < pre, x + shift behind it (shift 0 when the two ranges touch).
+// j = x for x < cut, x + shift behind it (shift 0 when the two ranges touch).
 // In the list's coordinates token i sees x < pre or xlo(i) <= x <= xhi(i).
+// With `align` above 1 (a power of two that divides the page size) every
+// aligned run of the list is an aligned run of slots, so the list also holds
+// the slots between pre and cut and up to align - 1 before lo: wanted() tells
+// them apart, and no token sees them.
 #pragma once
 
 #include "vx_paged.h"
@@ -17,24 +21,26 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kNoWindow = 1 << 30;
 
 struct KeyList {
-  int pre, shift, total;
+  int pre, lo, cut, shift, total;
 };
 
-__device__ __forceinline__ KeyList key_list(int i_first, int i_last, int window, int prefix, int kv) {
+__device__ __forceinline__ KeyList key_list(int i_first, int i_last, int window, int prefix, int kv, int align = 1) {
   KeyList k;
-  const int lo = min(max(0, i_first - window + 1), kv);
-  const int hi = min(i_last + 1, kv);
+  k.lo = min(max(0, i_first - window + 1), kv);
+  const int hi = min(i_last + 1, kv), lo = k.lo & -align;
   k.pre = min(max(prefix, 0), kv);
-  if (k.pre >= lo) {
+  k.cut = (k.pre + align - 1) & -align;
+  if (k.cut >= lo) {
     k.shift = 0;
     k.total = max(hi, k.pre);
   } else {
-    k.shift = lo - k.pre;
-    k.total = k.pre + max(hi - lo, 0);
+    k.shift = lo - k.cut;
+    k.total = k.cut + max(hi - lo, 0);
   }
   return k;
 }
-__device__ __forceinline__ int key_slot(const KeyList& k, int x) { return x + (x >= k.pre ? k.shift : 0); }
+__device__ __forceinline__ int key_slot(const KeyList& k, int x) { return x + (x >= k.cut ? k.shift : 0); }
+__device__ __forceinline__ bool wanted(const KeyList& k, int j) { return j < k.pre || j >= k.lo; }   // of x < total
 
 // 16 bytes global -> shared, or zeros when !valid (src must be readable all the same: it is not read).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {

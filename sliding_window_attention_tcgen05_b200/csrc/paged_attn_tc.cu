@@ -10,26 +10,34 @@ namespace {
 // range).  Rows are (token t, head g of the group), r = t * G + g, so a K/V
 // tile serves the group's heads at once; softmax warpgroup X owns rows
 // 128 X .. 128 X + 127 of the block (TMEM lane = row).  Keys are walked in
-// tiles of 128 of the block's key list.  Pages may have any size, so a tile's
-// rows lie anywhere: four producer warps copy them row by row with cp.async
-// into the 128-byte-swizzled layout the tensor core reads (rows past the
-// sequence as zeros), K and V tiles alternating in one ring.  One thread per
-// warpgroup issues S = Q K^T into TMEM, waits for P (written over S as bf16)
-// and issues O += P V; the two warpgroups' softmax phases and products
-// overlap.  O is rescaled in place only when a row's maximum grows by more
-// than 2^8.
-constexpr int kTcThreads = 512;   // 2 x 4 softmax warps, 4 producer warps, 2 issuers + 2 idle
+// tiles of 128 of the block's key list.  Pages may have any size and the list
+// may start anywhere in one, so a tile's rows lie anywhere: where the page size
+// is a multiple of 16 the list is cut into aligned runs of up to 128 rows that
+// lie in one page, and one producer warp for K and one for V fetch each run by
+// TMA; rows of a run that holds others than the block's keys, and all rows of
+// odd page sizes, are copied with cp.async into the same 128-byte-swizzled
+// layout (zeros for the others).  K and V tiles alternate in one ring.  One
+// thread per warpgroup issues O += P V as P arrives (written over S as bf16, 64
+// keys at a time), then the next S = Q K^T; the two threads take turns at the
+// second half of P V and S, which keeps the warpgroups out of step, so that
+// one's exponentials run under the other's products (left alone they fell into
+// step: 968 us for the 4 ragged prompts of 4096 tokens over 8192; with one
+// thread for both, whose own issue rate then counts, 937 us).
+// O is rescaled in place only when a row's maximum
+// grows by more than 2^8.
+constexpr int kTcThreads = 384;   // 2 x 4 softmax warps, 2 issuers, 2 producer warps
 constexpr int kTcKeys = 128;
 constexpr float kTcSlack = 8.0f;
-// setmaxnreg: 256 x 200 + 256 x 56 = the 512 x 128 of the launch.
-constexpr int kTcSoftmaxRegs = 200;
-constexpr int kTcOtherRegs = 56;
+// setmaxnreg: 256 x 216 + 128 x 72 = the 384 x 168 of the launch.  A row's 128
+// scores stay in registers (at 512 threads x 128 they spilled).
+constexpr int kTcSoftmaxRegs = 216;
+constexpr int kTcOtherRegs = 72;
 
 template <int D>
 struct TcCfg {
   static constexpr int kTile = kTcKeys * D * 2;               // one Q, K or V tile
   static constexpr int kStages = D == 128 ? 5 : 8;            // ring of K / V tiles
-  static constexpr int kLag = kStages - 2;                    // copies in flight behind the newest
+  static constexpr int kLag = 1;                              // a producer's cp.async tiles in flight behind the newest
   static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024 + 256;
 };
 
@@ -42,25 +50,69 @@ struct TcItem {
   SeqSpan q;
 };
 
-// The tile of keys [xt, xt + 128) meets what some row of warpgroup X sees.
-__device__ __forceinline__ bool tc_tile_used(const PagedAttnArgs& a, const TcItem& it, int X, int xt) {
+// The tiles first .. end - 1 of the CTA's that warpgroup X uses: the others,
+// at either end, hold no key that its rows see.
+struct TcTiles {
+  int first, end;
+};
+__device__ __forceinline__ TcTiles tc_tiles(const PagedAttnArgs& a, const TcItem& it, int X) {
   const int ra = it.r0 + X * 128, rz = min(ra + 127, it.rows - 1);
   const int i_first = it.q.old + static_cast<int>(a.group_div.div(ra));
   const int i_last = it.q.old + static_cast<int>(a.group_div.div(rz));
-  return xt < it.kl.pre || (xt <= i_last - it.kl.shift && xt + kTcKeys - 1 >= i_first - a.window + 1 - it.kl.shift);
+  const int lo = it.kl.pre > it.x0 ? it.x0 : max(it.x0, i_first - a.window + 1 - it.kl.shift);
+  const int hi = max(i_last - it.kl.shift, it.kl.pre - 1);   // last key seen
+  TcTiles t;
+  t.first = min((lo - it.x0) / kTcKeys, it.nt);
+  t.end = hi < it.x0 ? 0 : min((hi - it.x0) / kTcKeys + 1, it.nt);
+  t.end = max(t.end, t.first);
+  return t;
+}
+
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {   // does not wait
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
+// Packed fp32 pairs (each half rounds like the scalar operation) and the maximum of three.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 template <int D, bool MOD>
 __global__ void __launch_bounds__(kTcThreads, 1)
-paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ PagedAttnArgs a, int blocks, int run) {
   using Cfg = TcCfg<D>;
-  constexpr int NST = Cfg::kStages, LAG = Cfg::kLag, TILE = Cfg::kTile;
+  constexpr int NST = Cfg::kStages, TILE = Cfg::kTile;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                    // 2 tiles; a tile = D / 64 halves of [128 rows][128 bytes]
   uint8_t* sKV = smem + 2 * TILE;        // ring: K(0), V(0), K(1), V(1), ...
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + NST * TILE);
-  constexpr int FULL = 0, EMPTY = NST, SF = 2 * NST, PF = SF + 2, PVD = PF + 2, DR = PVD + 2, NBAR = DR + 2;
+  constexpr int FULL = 0, EMPTY = NST, SF = 2 * NST, PF = SF + 2, PVD = PF + 4, DR = PVD + 2, TK = DR + 2, QF = TK + 2, NBAR = QF + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_addr(bars + i); };
@@ -84,7 +136,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
   it.n_act = it.rows - it.r0 > 128 ? 2 : 1;
   {
     const int tf = a.group_div.div(it.r0), tl = a.group_div.div(min(it.r0 + 255, it.rows - 1));
-    it.kl = key_list(it.q.old + tf, it.q.old + tl, a.window, a.prefix ? a.prefix[it.s] : 0, it.q.kv);
+    it.kl = key_list(it.q.old + tf, it.q.old + tl, a.window, a.prefix ? a.prefix[it.s] : 0, it.q.kv, run);
     const int step = ((it.kl.total + a.splits - 1) / a.splits + kTcKeys - 1) / kTcKeys * kTcKeys;
     it.x0 = min(it.sp * step, it.kl.total);
     it.x1 = min(it.x0 + step, it.kl.total);
@@ -92,17 +144,20 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
   }
   if (threadIdx.x == 0) {
     if (it.q.over) report_bad_cache(a.status, it.s);
-    for (int i = 0; i < NST; ++i) { mbar_init(bar(FULL + i), 128); mbar_init(bar(EMPTY + i), it.n_act); }
+    for (int i = 0; i < NST; ++i) { mbar_init(bar(FULL + i), 32); mbar_init(bar(EMPTY + i), it.n_act); }
     for (int X = 0; X < 2; ++X) {
       mbar_init(bar(SF + X), 1);
-      mbar_init(bar(PF + X), 128);
+      mbar_init(bar(PF + 2 * X), 128);       // P of keys 0 .. 63 of the tile
+      mbar_init(bar(PF + 2 * X + 1), 128);   // and 64 .. 127
       mbar_init(bar(PVD + X), 1);
       mbar_init(bar(DR + X), 1);
+      mbar_init(bar(TK + X), 1);
     }
+    mbar_init(bar(QF), 64);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 8) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -115,18 +170,20 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
-    if (warp < 12) {
-      // ------------- producers: Q, then K(u), V(u) for every tile
-      constexpr int CPR = D / 8, RPI = 32 / CPR;   // 16-byte chunks of a row, rows per warp-wide copy
-      const int w = warp - 8, rbase = w * 32;      // this warp's 32 rows of every tile
-      const int c = lane % CPR;
+    if (warp >= 10) {
+      // ------------- producers: half of Q each, then warp 10 the K and warp 11 the V tiles
+      constexpr int CPR = D / 8, RPI = 32 / CPR;      // 16-byte chunks of a row, rows per warp-wide copy
+      const int c = lane % CPR, ch = c & 7, rl0 = lane / CPR;
       const uint32_t coff = (c >> 3) * (kTcKeys * 128);
-      const int ch = c & 7;
+      const bool is_v = warp == 11;
+      const CUtensorMap* tm = is_v ? &tmV : &tmK;
       const uint16_t* qp = static_cast<const uint16_t*>(a.q.p);
+      const uint8_t* pool = static_cast<const uint8_t*>(is_v ? a.v : a.k) + c * 16;
+      if (lane == 0) tma_prefetch_desc(tm);
       for (int X = 0; X < it.n_act; ++X) {
         const uint32_t dst = smem_addr(sQ + X * TILE) + coff;
-        for (int k = 0; k < 32 / RPI; ++k) {
-          const int r = rbase + k * RPI + lane / CPR;
+        for (int k = 0; k < 64 / RPI; ++k) {
+          const int r = (is_v ? 64 : 0) + k * RPI + rl0;
           const int rr = it.r0 + X * 128 + r;
           const bool ok = rr < it.rows;
           const int t = a.group_div.div(ok ? rr : 0), h = it.kh * a.group + (ok ? rr : 0) - t * a.group;
@@ -135,81 +192,169 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
         }
       }
       cp_async_commit();
-      auto lookup = [&](int u) -> int64_t {
-        const int x = it.x0 + u * kTcKeys + rbase + lane;
-        if (u >= it.nt || x >= it.x1) return -1;
-        const int64_t r = slot_row(a.c, it.s, it.kh, key_slot(it.kl, x));
-        if (r < 0) report_bad_cache(a.status, it.s);
-        return r;
-      };
-      int64_t row = 0, next = lookup(0);
-      const int nb = 2 * it.nt;
-      bool ok = true;
-      for (int b = 0; b < nb; ++b) {
-        const int st = b % NST;
-        const bool w_ok = mbar_wait(bar(EMPTY + st), ((b / NST) & 1) ^ 1, wc, 70);
-        if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-        if ((b & 1) == 0) {
-          row = next;
-          next = lookup(b / 2 + 1);
-        }
-        const uint16_t* pool = static_cast<const uint16_t*>((b & 1) ? a.v : a.k);
-        const uint32_t dst = smem_addr(sKV + st * TILE) + coff;
+      // Pool rows of four rows of tile u, or -1 (below 2^31, checked at launch): lane * 4 + k where runs are fetched
+      // by TMA (so that a run's rows are R / 4 neighbouring lanes'), else lane + 32 k.
+      const bool tma = run >= 16;
+      auto lookup = [&](int u, int (&row)[4]) {
 #pragma unroll
-        for (int k = 0; k < 32 / RPI; ++k) {
-          const int rl = k * RPI + lane / CPR, r = rbase + rl;
-          const int64_t gr = __shfl_sync(0xffffffffu, row, rl);
-          cp_async16(dst + r * 128 + ((ch ^ (r & 7)) << 4), pool + (gr < 0 ? 0 : gr) * D + c * 8, gr >= 0);
+        for (int k = 0; k < 4; ++k) {
+          const int x = it.x0 + u * kTcKeys + (tma ? lane * 4 + k : lane + 32 * k);
+          row[k] = -1;
+          if (u >= it.nt || x >= it.x1) continue;
+          const int j = key_slot(it.kl, x);
+          if (!wanted(it.kl, j)) continue;
+          row[k] = static_cast<int>(slot_row(a.c, it.s, it.kh, j));
+          if (row[k] < 0) report_bad_cache(a.status, it.s);
         }
-        cp_async_commit();
-        if (b >= LAG) {   // the buffer LAG back (and Q with the first) has landed
-          cp_async_wait<LAG>();
-          fence_proxy_async_smem();
-          mbar_arrive(bar(FULL + (b - LAG) % NST));
+      };
+      int row[4], next[4];
+      lookup(0, next);
+      int u = 0, told = 0;   // tiles issued, tiles whose arrival the consumers were told of (cp.async)
+      auto stage_of = [&](int v) { return (2 * v + (is_v ? 1 : 0)) % NST; };
+      auto landed = [&](int in_flight) {   // tile `told` (and Q before it) has landed once so many newer ones fly
+        if (in_flight >= 1) cp_async_wait<1>(); else cp_async_wait<0>();
+        fence_proxy_async_smem();
+        if (told == 0) mbar_arrive(bar(QF));
+        mbar_arrive(bar(FULL + stage_of(told)));
+        ++told;
+      };
+      for (; u < it.nt; ++u) {
+        const int st = stage_of(u);
+        const uint32_t full = bar(FULL + st), dst = smem_addr(sKV + st * TILE);
+        const uint32_t empty = (((2 * u + (is_v ? 1 : 0)) / NST) & 1) ^ 1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) row[k] = next[k];
+        lookup(u + 1, next);
+        // No free buffer: nothing to issue, so pass on what lands meanwhile.
+        if (!tma)
+          while (told < u && !__all_sync(0xffffffffu, mbar_test_wait(bar(EMPTY + st), empty))) landed(u - told - 1);
+        const bool w_ok = mbar_wait(bar(EMPTY + st), empty, wc, 70);
+        if (!__all_sync(0xffffffffu, w_ok)) break;
+        if (tma) {
+          const uint32_t have = __ballot_sync(0xffffffffu, min(min(row[0], row[1]), min(row[2], row[3])) >= 0);
+          const int lanes = run / 4;                                   // of a run
+          const uint32_t mine = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (lane & -lanes);
+          const bool whole = (have & mine) == mine;
+          const uint32_t runs = __ballot_sync(0xffffffffu, whole);     // a bit for each lane of a whole run
+          if (lane == 0) mbar_arrive_expect_tx(full, __popc(runs) * (4 * D * 2));
+          __syncwarp();
+          if (whole && (lane & (lanes - 1)) == 0)
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+              tma_load_2d(dst + hf * (kTcKeys * 128) + lane * 512, tm, full, hf * 64, row[0]);
+          if (runs != 0xffffffffu) {
+            for (int k = 0; k < 128 / RPI; ++k) {
+              const int r = k * RPI + rl0;
+              if ((runs >> (k * RPI / 4)) & 1u) continue;              // a warp-wide copy lies in one run
+              int gr = -1;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int y = __shfl_sync(0xffffffffu, row[j], r >> 2);
+                if ((r & 3) == j) gr = y;
+              }
+              cp_async16(dst + coff + r * 128 + ((ch ^ (r & 7)) << 4),
+                         pool + static_cast<int64_t>(max(gr, 0)) * (2 * D), gr >= 0);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+          }
+          if (lane != 0) mbar_arrive(full);
+          if (u == 0) {   // Q, copied before the first tile
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            mbar_arrive(bar(QF));
+          }
+        } else {
+#pragma unroll
+          for (int k0 = 0; k0 < 128 / RPI; k0 += 8) {   // eight rows' numbers first: a shuffle before each copy takes 75 cycles a copy
+            int gr[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              gr[k] = __shfl_sync(0xffffffffu, row[(k0 + k) * RPI / 32], ((k0 + k) * RPI + rl0) & 31);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = (k0 + k) * RPI + rl0;
+              cp_async16(dst + coff + r * 128 + ((ch ^ (r & 7)) << 4),
+                         pool + static_cast<int64_t>(max(gr[k], 0)) * (2 * D), gr[k] >= 0);
+            }
+          }
+          cp_async_commit();
+          if (u - told >= Cfg::kLag) landed(Cfg::kLag);
         }
       }
+      while (!tma && u == it.nt && told < u) landed(u - told - 1);
       cp_async_wait<0>();
-      fence_proxy_async_smem();
-      if (ok)
-        for (int b = max(0, nb - LAG); b < nb; ++b) mbar_arrive(bar(FULL + b % NST));
-    } else if (warp < 14 && lane == 0 && warp - 12 < it.n_act) {
+      if (tma && u < it.nt) {   // gave up: the copies in flight must land before the CTA ends
+        int zero = 0;
+        WaitCtx dw = wc;
+        dw.abort_flag = &zero;
+        for (int v = max(0, u - NST / 2 - 1); v < u; ++v) {
+          const int b = 2 * v + (is_v ? 1 : 0);
+          mbar_wait(bar(FULL + b % NST), (b / NST) & 1, dw, 80);
+        }
+      }
+    } else if (lane == 0 && warp - 8 < it.n_act) {
       // ------------- tensor-core products of warpgroup X
-      const int X = warp - 12;
+      const int X = warp - 8;
       const uint32_t tS = tmem + X * 128, tO = tmem + 256 + X * D;
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTcKeys, 0);
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, 1);
-      const uint32_t qa = smem_addr(sQ + X * TILE);
-      int t = 0;
-      bool ok = true;
-      for (int u = 0; ok && u < it.nt; ++u) {
-        const int bk = 2 * u, bv = bk + 1, sk = bk % NST, sv = bv % NST;
-        if (!(ok = mbar_wait(bar(FULL + sk), (bk / NST) & 1, wc, 71))) break;
-        const bool used = tc_tile_used(a, it, X, it.x0 + u * kTcKeys);
-        if (!used) {
-          mbar_arrive(bar(EMPTY + sk));
-          if (!(ok = mbar_wait(bar(FULL + sv), (bv / NST) & 1, wc, 72))) break;
+      const TcTiles tiles = tc_tiles(a, it, X);
+      // Descriptors of the first tiles; a stage or a K step further is an addition to the address field (built anew
+      // for each product they take longer than the product).
+      const uint64_t desc_q = smem_desc_sw128(smem_addr(sQ + X * TILE), 16, 1024);
+      const uint64_t desc_k = smem_desc_sw128(smem_addr(sKV), 16, 1024);
+      const uint64_t desc_v = smem_desc_sw128(smem_addr(sKV), kTcKeys * 128, 1024);
+      const bool both = it.n_act == 2;
+      bool ok = it.nt == 0 || mbar_wait(bar(QF), 0, wc, 79);
+      for (int u = -1; ok && u < it.nt; ++u) {   // O += P V of tile u, then S of tile u + 1
+        const int bk = 2 * u + 2, bv = 2 * u + 1, sk = bk % NST, sv = bv % NST, t = u - tiles.first;
+        const bool pv = u >= tiles.first && u < tiles.end, sc = u + 1 >= tiles.first && u + 1 < tiles.end;
+        const uint64_t dv = desc_v + static_cast<uint32_t>(sv * (TILE >> 4));
+        auto half_pv = [&](int half) {
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {   // 16 keys: 8 TMEM columns of P, 16 rows of V
+            const int kk = half * 4 + k4;
+            umma_bf16_ts(tO, tS + 8 * kk, dv + kk * (2048 >> 4), idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
+          }
+        };
+        if (u >= 0 && !(ok = mbar_wait(bar(FULL + sv), (bv / NST) & 1, wc, 73))) break;
+        if (pv) {
+          if (!(ok = mbar_wait(bar(PF + 2 * X), t & 1, wc, 74))) break;
+          tc_fence_after();
+          half_pv(0);
+        } else if (u >= 0) {
           mbar_arrive(bar(EMPTY + sv));
-          continue;
         }
+        if (u + 1 < it.nt && !(ok = mbar_wait(bar(FULL + sk), (bk / NST) & 1, wc, 71))) break;
+        if (pv && !(ok = mbar_wait(bar(PF + 2 * X + 1), t & 1, wc, 74))) break;
+        if (both && !(ok = mbar_wait(bar(TK + X), (u & 1) ^ X, wc, 72))) break;
         tc_fence_after();
-        const uint32_t ka = smem_addr(sKV + sk * TILE), va = smem_addr(sKV + sv * TILE);
+        if (pv) half_pv(1);
+        if (sc) {   // S(u + 1) overwrites P(u), which the product before it has read
+          const uint64_t dk = desc_k + static_cast<uint32_t>(sk * (TILE >> 4));
+          if (pv) {
+            umma_commit(bar(PVD + X));
+            umma_commit(bar(EMPTY + sv));
+          }
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {   // S(t) overwrites P(t - 1), which the product before it has read
-          const uint32_t o = (kk >> 2) * (kTcKeys * 128) + (kk & 3) * 32;
-          umma_bf16(tS, smem_desc_sw128(qa + o, 16, 1024), smem_desc_sw128(ka + o, 16, 1024), idesc_s, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = ((kk >> 2) * (kTcKeys * 128) + (kk & 3) * 32) >> 4;
+            umma_bf16(tS, desc_q + o, dk + o, idesc_s, kk > 0);
+          }
         }
-        umma_commit(bar(SF + X));
-        umma_commit(bar(EMPTY + sk));
-        if (!(ok = mbar_wait(bar(FULL + sv), (bv / NST) & 1, wc, 73))) break;
-        if (!(ok = mbar_wait(bar(PF + X), t & 1, wc, 74))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kTcKeys / 16; ++kk)   // 16 keys: 8 TMEM columns of P, 16 rows of V
-          umma_bf16_ts(tO, tS + 8 * kk, smem_desc_sw128(va + kk * 2048, kTcKeys * 128, 1024), idesc_o,
-                       (t > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(bar(PVD + X));
-        umma_commit(bar(EMPTY + sv));
-        ++t;
+        if (both) mbar_arrive(bar(TK + (X ^ 1)));
+        if (sc) {
+          umma_commit(bar(SF + X));
+          umma_commit(bar(EMPTY + sk));
+        } else {
+          if (pv) {
+            umma_commit(bar(PVD + X));
+            umma_commit(bar(EMPTY + sv));
+          }
+          if (u + 1 < it.nt) mbar_arrive(bar(EMPTY + sk));
+        }
       }
       umma_commit(bar(DR + X));
       int zero = 0;
@@ -234,20 +379,22 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
       const int xlo = max(0, i - a.window + 1 - it.kl.shift), xhi = min(i - it.kl.shift, it.x1 - 1);
       const int pre = min(it.kl.pre, it.x1);
       const int all_lo = __reduce_max_sync(0xffffffffu, xlo), all_hi = __reduce_min_sync(0xffffffffu, xhi);
+      const TcTiles tiles = tc_tiles(a, it, X);
       float m_used = -INFINITY, l_run = 0.f;
       int t = 0;
       bool ok = true;
-      for (int u = 0; u < it.nt; ++u) {
+      for (int u = tiles.first; u < tiles.end; ++u) {
         const int xt = it.x0 + u * kTcKeys;
-        if (!tc_tile_used(a, it, X, xt)) continue;
         bool w = mbar_wait(bar(SF + X), t & 1, wc, 76);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         tc_fence_after();
         float sv[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t(&rr)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c);
+          uint32_t rr[32];
           tmem_ld32(tS + 32 * c, rr);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sv[32 * c + e] = __uint_as_float(rr[e]);
         }
         tmem_ld_wait();
         if constexpr (MOD) {
@@ -256,16 +403,23 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
         }
         if (!((xt >= all_lo && xt + kTcKeys - 1 <= all_hi) || xt + kTcKeys - 1 < pre)) {
           const int lo = xlo - xt, hi = xhi - xt, pr = pre - xt;
+          if (pr <= 0 && xt >= all_lo) {   // only the causal edge (or the list's end)
 #pragma unroll
-          for (int e = 0; e < 128; ++e) sv[e] = ((e >= lo && e <= hi) || e < pr) ? sv[e] : -INFINITY;
+            for (int e = 0; e < 128; ++e) sv[e] = e <= hi ? sv[e] : -INFINITY;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 128; ++e) sv[e] = ((e >= lo && e <= hi) || e < pr) ? sv[e] : -INFINITY;
+          }
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-        for (int e = 0; e < 128; e += 4)
+        for (int e = 4; e < 124; e += 8)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], sv[e + k]);
+          for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], sv[e + 2 * k], sv[e + 2 * k + 1]);
+        mx[0] = fmax3(mx[0], sv[124], sv[125]);
+        mx[1] = fmax3(mx[1], sv[126], sv[127]);
         const float sc = MOD ? 1.f : sm.sl2;
-        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const float m_tile = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sc;
         float corr = 1.f;
         if (m_tile > m_used + kTcSlack) {
           if (m_used != -INFINITY) corr = ex2_approx(m_used - m_tile);
@@ -287,23 +441,28 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
           }
         }
         const float mu = m_used == -INFINITY ? 0.f : m_used;
-        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sc2 = f2_pack(sc, sc), mu2 = f2_pack(-mu, -mu);
+        uint64_t rs[2] = {0, 0};   // two packed sums
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float p0 = ex2_approx(fmaf(sv[c * 64 + 2 * e], sc, -mu));
-            const float p1 = ex2_approx(fmaf(sv[c * 64 + 2 * e + 1], sc, -mu));
-            rs[e & 3] += p0 + p1;
+            float p0, p1;
+            f2_unpack(ffma2(f2_pack(sv[c * 64 + 2 * e], sv[c * 64 + 2 * e + 1]), sc2, mu2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            rs[e & 1] = fadd2(rs[e & 1], f2_pack(p0, p1));
             pk[e] = pack_bf16x2(p0, p1);
           }
           tmem_st32(tS + 32 * c, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar(PF + 2 * X + c));
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar(PF + X));
-        l_run += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+        float r0, r1;
+        f2_unpack(fadd2(rs[0], rs[1]), r0, r1);
+        l_run += r0 + r1;
         ++t;
       }
       if (ok && t > 0) {
@@ -352,7 +511,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
     }
   }
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -360,9 +519,22 @@ paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
 
 template <int D, bool MOD>
 cudaError_t launch_tc(const Launch& L, const PagedAttnArgs& a, int blocks) {
+  const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) * a.c.n_heads * a.c.page.d;
+  if (rows >= 1ull << 31) return cudaErrorInvalidValue;   // a row's number is a 32-bit coordinate (256 GB of K at D = 64)
+  CUtensorMap tk, tv;
+  const uint64_t dims[2] = {D, rows}, strides[1] = {D * 2};
+  // Runs: the largest power of two that divides the page size, up to a tile.  Below 16 rows a TMA copy each costs more
+  // than copying the rows with cp.async.
+  int run = 1;
+  while (run < kTcKeys && a.c.page.d % (2 * run) == 0) run *= 2;
+  if (run < 16) run = 1;
+  const uint32_t box[2] = {64, static_cast<uint32_t>(run)};
+  if (!encode_tmap(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(blocks) * a.c.n_seqs * a.c.n_heads * a.splits);
-  return launch_kernel(paged_attn_tc_kernel<D, MOD>, dim3(grid), dim3(kTcThreads), TcCfg<D>::kSmem, L.stream, a,
-                       blocks);
+  return launch_kernel(paged_attn_tc_kernel<D, MOD>, dim3(grid), dim3(kTcThreads), TcCfg<D>::kSmem, L.stream, tk, tv, a,
+                       blocks, run);
 }
 
 }  // namespace

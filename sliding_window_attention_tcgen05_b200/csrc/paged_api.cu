@@ -43,6 +43,13 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
   if (sp > most) sp = most;
   if (sp > kMaxSplits) sp = kMaxSplits;
   p.splits = static_cast<int>(sp < 1 ? 1 : sp);
+  // Sum of the weights: segments until there are a few CTAs for each place on the SMs (8 of 128 threads each), none
+  // below four blocks of 64 rows.
+  const int64_t w_ctas = lanes * ((max_kv + 63) / 64), most_segs = rows / 256;
+  int64_t segs = (3 * 8 * kPlanSms + w_ctas - 1) / w_ctas;
+  if (segs > most_segs) segs = most_segs;
+  if (segs > 32) segs = 32;
+  p.w_segs = static_cast<int>(segs < 1 ? 1 : segs);
   return p;
 }
 
@@ -162,16 +169,20 @@ struct AttnCarve {
   float* lse;
   float* part_o;
   float2* part_ml;
+  float* part_w;
 };
-AttnCarve carve_attn(Carve& cv, int64_t n_tokens, int n_q_heads, int head_dim, int splits, bool own_lse) {
-  AttnCarve r = {nullptr, nullptr, nullptr};
+AttnCarve carve_attn(Carve& cv, const vx_paged_cache* c, int64_t n_tokens, int n_q_heads, const PagedAttnPlan& p,
+                     int64_t max_kv, bool lse, bool track) {
+  AttnCarve r = {};
   const int64_t rows = n_tokens * n_q_heads;
   cv.take(kStatusBytes);
-  if (own_lse) r.lse = static_cast<float*>(cv.take(rows * 4));
-  if (splits > 1) {
-    r.part_o = static_cast<float*>(cv.take(rows * splits * head_dim * 4));
-    r.part_ml = static_cast<float2*>(cv.take(rows * splits * 8));
+  if (track && !lse) r.lse = static_cast<float*>(cv.take(rows * 4));
+  if (p.splits > 1) {
+    r.part_o = static_cast<float*>(cv.take(rows * p.splits * c->head_dim * 4));
+    r.part_ml = static_cast<float2*>(cv.take(rows * p.splits * 8));
   }
+  if (track && p.w_segs > 1)
+    r.part_w = static_cast<float*>(cv.take(max_kv * p.w_segs * c->n_seqs * c->n_kv_heads * 4));
   return r;
 }
 
@@ -297,10 +308,11 @@ size_t vx_paged_attn_workspace(const vx_paged_cache* cache, int n_q_heads, int64
   const int mq = static_cast<int>(max_q < n_tokens ? max_q : n_tokens);
   const int group = n_q_heads / cache->n_kv_heads;
   if (mq == 0 || group < 1) return kAlign;
+  const int64_t kv = bound_kv(cache, max_kv);
   const PagedAttnPlan p = plan_paged_attn(cache->dt == VX_BF16, cache->head_dim, cache->n_seqs, cache->n_kv_heads,
-                                          group, mq, bound_kv(cache, max_kv));
+                                          group, mq, kv);
   Carve cv{nullptr, 0};
-  carve_attn(cv, n_tokens, n_q_heads, cache->head_dim, p.splits, track && !want_lse);
+  carve_attn(cv, cache, n_tokens, n_q_heads, p, kv, want_lse, track);
   return align_up(cv.off, kAlign);
 }
 
@@ -331,10 +343,10 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
                what);
   const bool bf16 = cache->dt == VX_BF16;
   const int64_t kv = bound_kv(cache, max_kv);
-  PagedAttnPlan plan = {0, 1};
+  PagedAttnPlan plan = {0, 1, 1};
   if (mq > 0) plan = plan_paged_attn(bf16, cache->head_dim, cache->n_seqs, cache->n_kv_heads, group, mq, kv);
   Carve cv{static_cast<uint8_t*>(ws), 0};
-  const AttnCarve bf = carve_attn(cv, n_tokens, n_q_heads, cache->head_dim, plan.splits, track && !lse);
+  const AttnCarve bf = carve_attn(cv, cache, n_tokens, n_q_heads, plan, kv, lse != nullptr, track != 0);
   Launch L;
   if ((st = make_launch(&L, ws, ws_bytes, mq > 0 ? cv.off : kStatusBytes, stream)) != VX_OK) return st;
   if (mq == 0) return VX_OK;
@@ -366,6 +378,9 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
   a.splits = plan.splits;
   a.part_o = bf.part_o;
   a.part_ml = bf.part_ml;
+  a.w_segs = plan.w_segs;
+  a.part_w = bf.part_w;
+  a.part_stride = kv;
   a.status = L.status;
   a.limit_ns = L.limit_ns;
   const int64_t rows = static_cast<int64_t>(mq) * group;
@@ -379,7 +394,7 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
   if (plan.splits > 1)
     VX_CUDA(traced(L, "paged_attn_combine", 1, [&] { return launch_paged_attn_combine(L, a, bf16); }));
   if (track)
-    VX_CUDA(traced(L, "paged_attn_weights", 1, [&] { return launch_paged_attn_weights(L, a, bf16, kv); }));
+    VX_CUDA(traced(L, "paged_attn_weights", plan.w_segs > 1 ? 2 : 1, [&] { return launch_paged_attn_weights(L, a, bf16, kv); }));
   return VX_OK;
 }
 

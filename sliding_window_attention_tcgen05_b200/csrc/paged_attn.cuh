@@ -79,21 +79,46 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // Scores to the exponent's base-2 units.  Without cap and slopes that is one
 // multiplication by scale * log2(e).  cap * tanh(z) = cap * (1 - 2 / (e^{2z} + 1)),
-// from one exponential and one reciprocal (absolute error about cap * 2^-23,
+// from one exponential and half a reciprocal (absolute error about cap * 2^-22,
 // where the hardware's own tanh would leave cap * 2^-11).
 struct ScoreMod {
   float sl2;       // scale * log2 e
   float cap2;      // cap * log2 e, 0 = no cap
   float two_z;     // 2 scale / cap * log2 e
+  bool bias;       // slopes
 };
 __device__ __forceinline__ ScoreMod score_mod(const PagedAttnArgs& a) {
   ScoreMod m;
   m.sl2 = a.scale * kLog2e;
   m.cap2 = a.cap * kLog2e;
   m.two_z = a.cap > 0.f ? 2.f * a.scale / a.cap * kLog2e : 0.f;
+  m.bias = a.slopes != nullptr;
   return m;
 }
-// slope2 = slope of the head * log2 e, dist = |i - j|
+__device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either is
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// N raw scores, two at a time: 1 / a and 1 / b from one reciprocal of a b (exponents up to 2^60, beyond which tanh is 1
+// to the last bit, so that the product stays finite).
+template <int N>
+__device__ __forceinline__ void scale_scores(const ScoreMod& m, float (&s)[N]) {
+  if (m.cap2 > 0.f) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float a = ex2_approx(min_nan(s[e] * m.two_z, 60.f)) + 1.f;
+      const float b = ex2_approx(min_nan(s[e + 1] * m.two_z, 60.f)) + 1.f;
+      const float r = -2.f * m.cap2 * rcp_approx(a * b);
+      s[e] = fmaf(r, b, m.cap2);
+      s[e + 1] = fmaf(r, a, m.cap2);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e] *= m.sl2;
+  }
+}
+// slope2 = slope of the head * log2 e, dist = i - j
 __device__ __forceinline__ float score2(const ScoreMod& m, float s, float slope2, int dist) {
   float y;
   if (m.cap2 > 0.f) {
@@ -102,7 +127,7 @@ __device__ __forceinline__ float score2(const ScoreMod& m, float s, float slope2
   } else {
     y = s * m.sl2;
   }
-  return y - slope2 * static_cast<float>(dist);
+  return y - slope2 * static_cast<float>(abs(dist));
 }
 
 cudaError_t launch_paged_attn_rows(const Launch& L, const PagedAttnArgs& a);

@@ -1,6 +1,8 @@
 // paged_attn_rows.cu -- attention over the paged cache for few query rows
 // (decoding, streaming steps), its fp32 form, the joining of split key ranges
 // and the accumulated attention weights.
+#include <type_traits>
+
 #include "paged_attn.cuh"
 
 namespace vx {
@@ -152,13 +154,16 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float cmax = -INFINITY;
+          float y[4] = {sa[mt][0][2 * half], sa[mt][0][2 * half + 1], sa[mt][1][2 * half], sa[mt][1][2 * half + 1]};
+          if constexpr (MOD) scale_scores(sm, y);
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float& v = sa[mt][nb][2 * half + e];
               const int x = xb + nb * 8 + qc + e;
-              v = MOD ? score2(sm, v, slope2[mt][half], abs(qi[mt][half] - key_slot(kl, x))) : v * sm.sl2;
+              v = MOD ? y[2 * nb + e] : v * sm.sl2;
+              if (MOD && sm.bias) v -= slope2[mt][half] * static_cast<float>(abs(qi[mt][half] - key_slot(kl, x)));
               if (!clean) v = (x < pre || (x >= xlo[mt][half] && x <= xhi[mt][half] && x < x1)) ? v : -INFINITY;
               cmax = fmaxf(cmax, v);
             }
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool seen = x < x1 && (js < kl.pre || (js <= qi[j] && js > qi[j] - a.window));
-      const float v = seen ? score2(sm, dot[j], slope2[j], abs(qi[j] - js)) : -INFINITY;
+      const float v = seen ? score2(sm, dot[j], slope2[j], qi[j] - js) : -INFINITY;
       float cmax = v;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, off));
@@ -474,9 +479,23 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
 // Accumulated weights: acc_j = decay * acc_j + sum over the chunk's rows of
 // exp(s - lse).  The keys are the M side (K fragments stay in registers), the
 // rows stream past in blocks of 64, so every slot's sum stays in one thread
-// group's registers: no atomics, a fixed order.
+// group's registers: no atomics, a fixed order.  CTA per (64 slots x segment
+// of their row blocks, K/V head, sequence): early slots are seen by all rows
+// and late ones by few, and cutting the rows into segments evens that out (8
+// ragged chunks of 1500 tokens, 12 heads: 465 us without segments).  Segments'
+// sums go to the workspace and are added up by paged_attn_weights_sum_kernel.
+// Slots from part_stride on (a caller's max_kv that was too low) are left to
+// the first segment, which then takes all their rows.
 constexpr int kWKeys = 64;
 constexpr int kWRows = 64;
+
+// acc of slot j's row: decay * acc + x.
+__device__ __forceinline__ void add_weight(const PagedAttnArgs& a, int64_t row, float x) {
+  if (row >= 0) a.acc[row] = (a.acc_decay != 0.f ? a.acc_decay * a.acc[row] : 0.f) + x;
+}
+__device__ __forceinline__ float* weight_part(const PagedAttnArgs& a, int seg, int s, int kh) {
+  return a.part_w + ((static_cast<int64_t>(seg) * a.c.n_seqs + s) * a.c.n_heads + kh) * a.part_stride;
+}
 
 template <int D, bool MOD>
 __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_constant__ PagedAttnArgs a) {
@@ -487,9 +506,10 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
   const uint32_t sk = smem_addr(smem);
   const uint32_t sq0 = sk + kWKeys * 2 * D;
   float* s_lse = reinterpret_cast<float*>(smem + (kWKeys + 2 * kWRows) * 2 * D);   // [2][64]
-  int* s_i = reinterpret_cast<int*>(s_lse + 2 * kWRows);                          // [2][64]
-  float* s_sl = reinterpret_cast<float*>(s_i + 2 * kWRows);                       // [2][64]
+  float* s_sl = s_lse + 2 * kWRows;                                               // [2][64]
+  int* s_i = reinterpret_cast<int*>(s_sl + 2 * kWRows);                           // [2][64]: i - first slot of the tile
   const int kh = blockIdx.y, s = blockIdx.z;
+  const int seg = blockIdx.x % a.w_segs, tile0 = blockIdx.x / a.w_segs, tiles = gridDim.x / a.w_segs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const SeqSpan q = seq_span(a.c, a.ch, s);
   if (q.n <= 0) return;
@@ -498,13 +518,21 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
   const ScoreMod sm = score_mod(a);
   const uint16_t* kp = static_cast<const uint16_t*>(a.k);
   const uint16_t* qp = static_cast<const uint16_t*>(a.q.p);
-  for (int tile = blockIdx.x; tile * kWKeys < q.kv; tile += gridDim.x) {
+  for (int tile = tile0; tile * kWKeys < q.kv; tile += tiles) {
     const int j0 = tile * kWKeys, j1 = min(j0 + kWKeys, q.kv);
+    const bool cut = a.w_segs > 1 && j1 <= a.part_stride;
+    if (!cut && seg > 0) continue;
     // Tokens that see some slot of the tile.
     int t0 = max(0, j0 - q.old);
     int t1 = min(q.n, j1 - 1 - q.old + min(a.window, kNoWindow - 1 - j1));
     if (j0 < pre) { t0 = 0; t1 = q.n; }
-    const int ra = t0 * G, rz = max(t1 * G, ra);
+    int ra = t0 * G, rz = max(t1 * G, ra);
+    if (cut) {
+      const int64_t all = (rz - ra + kWRows - 1) / kWRows;
+      const int b0 = static_cast<int>(all * seg / a.w_segs), b1 = static_cast<int>(all * (seg + 1) / a.w_segs);
+      rz = min(rz, ra + b1 * kWRows);
+      ra += b0 * kWRows;
+    }
     auto stage_q = [&](int blk, int buf) {
       const int rbase = ra + blk * kWRows;
       for (int i = tid; i < kWRows * CPR; i += 128) {
@@ -519,18 +547,20 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
         const int t = a.group_div.div(ok ? rbase + tid : 0), h = kh * G + (ok ? rbase + tid : 0) - t * G;
         const float z = ok ? a.lse[static_cast<int64_t>(q.row0 + t) * a.n_q_heads + h] : -INFINITY;
         s_lse[buf * kWRows + tid] = z == -INFINITY ? INFINITY : z * kLog2e;   // weight 0 without a sum
-        s_i[buf * kWRows + tid] = q.old + t;
-        s_sl[buf * kWRows + tid] = a.slopes ? a.slopes[h] * kLog2e : 0.f;
+        s_i[buf * kWRows + tid] = q.old + t - j0;
+        s_sl[buf * kWRows + tid] = MOD && a.slopes ? a.slopes[h] * kLog2e : 0.f;
       }
       cp_async_commit();
     };
     const int blocks = (rz - ra + kWRows - 1) / kWRows;
-    for (int i = tid; i < kWKeys * CPR; i += 128) {
-      const int r = i / CPR, c = i % CPR;
-      const int64_t gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
-      cp_async16(sk + r * 2 * D + ((c ^ (r & 7)) << 4), kp + (gr < 0 ? 0 : gr) * D + c * 8, gr >= 0);
+    if (blocks > 0) {
+      for (int i = tid; i < kWKeys * CPR; i += 128) {
+        const int r = i / CPR, c = i % CPR;
+        const int64_t gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
+        cp_async16(sk + r * 2 * D + ((c ^ (r & 7)) << 4), kp + (gr < 0 ? 0 : gr) * D + c * 8, gr >= 0);
+      }
+      stage_q(0, 0);
     }
-    if (blocks > 0) stage_q(0, 0); else cp_async_commit();
     cp_async_wait<0>();
     __syncthreads();
     // This warp's 16 keys as A fragments: ldmatrix x4 = rows 0-7 / 8-15 at dims 0-7 / 8-15.
@@ -541,7 +571,9 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
       for (int ks = 0; ks < D / 16; ++ks)
         ldsm_x4(sk + r * 2 * D + (((ks * 2 + (lane >> 4)) ^ (r & 7)) << 4), ka[ks][0], ka[ks][1], ka[ks][2], ka[ks][3]);
     }
-    const int jr[2] = {j0 + warp * 16 + (lane >> 2), j0 + warp * 16 + (lane >> 2) + 8};
+    const int jr[2] = {warp * 16 + (lane >> 2), warp * 16 + (lane >> 2) + 8};   // from j0
+    const float jf[2] = {static_cast<float>(jr[0]), static_cast<float>(jr[1])};
+    const int pr = pre - j0;
     float sum[2] = {0.f, 0.f};
     for (int blk = 0; blk < blocks; ++blk) {
       const int buf = blk & 1;
@@ -551,9 +583,13 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
       }
       if (blk + 1 < blocks) stage_q(blk + 1, buf ^ 1);
       const uint32_t sq = sq0 + buf * kWRows * 2 * D;
-#pragma unroll 2
-      for (int nb = 0; nb < kWRows / 8; ++nb) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+      // Whether all rows of the block see all keys of the tile.
+      const int r_first = ra + blk * kWRows, r_last = min(r_first + kWRows, rz) - 1;
+      const int i_first = q.old + static_cast<int>(a.group_div.div(r_first)) - j0;
+      const int i_last = q.old + static_cast<int>(a.group_div.div(r_last)) - j0;
+      const bool clean = (i_first >= kWKeys - 1 && i_last - a.window < 0) || pr >= kWKeys;
+      auto rows8 = [&](int nb, auto masked) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};   // keys jr[0] (0, 1) and jr[1] (2, 3), rows col, col + 1
         const int r = nb * 8 + (lane & 7);
 #pragma unroll
         for (int h = 0; h < D / 32; ++h) {
@@ -563,18 +599,38 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
           mma_bf16_16816(c, ka[2 * h + 1][0], ka[2 * h + 1][1], ka[2 * h + 1][2], ka[2 * h + 1][3], b2, b3);
         }
         const int col = buf * kWRows + nb * 8 + (lane & 3) * 2;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float z = s_lse[col + e];
-          const int i = s_i[col + e];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int j = jr[half];
-            const float v = MOD ? score2(sm, c[2 * half + e], s_sl[col + e], abs(i - j)) : c[2 * half + e] * sm.sl2;
-            const bool seen = j < pre || (j <= i && j > i - a.window);
-            sum[half] += seen ? ex2_approx(v - z) : 0.f;
+        const float2 z = *reinterpret_cast<const float2*>(s_lse + col);
+        if constexpr (MOD) {
+          scale_scores(sm, c);
+          if (sm.bias) {
+            const float2 sl = *reinterpret_cast<const float2*>(s_sl + col);
+            const int2 i = *reinterpret_cast<const int2*>(s_i + col);
+            const float i0 = static_cast<float>(i.x), i1 = static_cast<float>(i.y);
+            c[0] = fmaf(-sl.x, fabsf(i0 - jf[0]), c[0]);
+            c[1] = fmaf(-sl.y, fabsf(i1 - jf[0]), c[1]);
+            c[2] = fmaf(-sl.x, fabsf(i0 - jf[1]), c[2]);
+            c[3] = fmaf(-sl.y, fabsf(i1 - jf[1]), c[3]);
           }
         }
+        const float sc = MOD ? 1.f : sm.sl2;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float p0 = ex2_approx(fmaf(c[2 * half], sc, -z.x)), p1 = ex2_approx(fmaf(c[2 * half + 1], sc, -z.y));
+          if constexpr (decltype(masked)::value) {
+            const int2 i = *reinterpret_cast<const int2*>(s_i + col);
+            const int j = jr[half];
+            p0 = (j < pr || (j <= i.x && j > i.x - a.window)) ? p0 : 0.f;
+            p1 = (j < pr || (j <= i.y && j > i.y - a.window)) ? p1 : 0.f;
+          }
+          sum[half] += p0 + p1;
+        }
+      };
+      if (clean) {
+#pragma unroll 4
+        for (int nb = 0; nb < kWRows / 8; ++nb) rows8(nb, std::false_type{});
+      } else {
+#pragma unroll 2
+        for (int nb = 0; nb < kWRows / 8; ++nb) rows8(nb, std::true_type{});
       }
     }
 #pragma unroll
@@ -582,16 +638,33 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
       float x = sum[half];
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       x += __shfl_xor_sync(0xffffffffu, x, 2);
-      if ((lane & 3) == 0 && jr[half] < j1) {
-        const int64_t row = slot_row(a.c, s, kh, jr[half]);
-        if (row >= 0) a.acc[row] = (a.acc_decay != 0.f ? a.acc_decay * a.acc[row] : 0.f) + x;
+      if ((lane & 3) == 0 && j0 + jr[half] < j1) {
+        if (cut) weight_part(a, seg, s, kh)[j0 + jr[half]] = x;
+        else add_weight(a, slot_row(a.c, s, kh, j0 + jr[half]), x);
       }
     }
     __syncthreads();   // the tile's buffers are refilled
   }
 }
 
-// fp32: CTA per 32 slots; a lane owns a slot, each warp every fourth row.
+// Adds up the segments' sums.
+__global__ void __launch_bounds__(128) paged_attn_weights_sum_kernel(const __grid_constant__ PagedAttnArgs a, int keys) {
+  pdl_wait();
+  pdl_trigger();
+  const int kh = blockIdx.y, s = blockIdx.z;
+  const SeqSpan q = seq_span(a.c, a.ch, s);
+  if (q.n <= 0) return;
+  const int j = static_cast<int>(blockIdx.x) * 128 + threadIdx.x;
+  const int tile_end = min((j / keys + 1) * keys, q.kv);   // as the segments saw it
+  if (j >= q.kv || tile_end > a.part_stride) return;
+  float x = 0.f;
+  for (int seg = 0; seg < a.w_segs; ++seg) x += weight_part(a, seg, s, kh)[j];
+  add_weight(a, slot_row(a.c, s, kh, j), x);
+}
+
+// fp32: CTA per 32 slots (and segment of their rows); a lane owns a slot, each warp every fourth row.
+constexpr int kWKeysF32 = 32;
+
 template <int D>
 __global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __grid_constant__ PagedAttnArgs a) {
   pdl_wait();
@@ -601,14 +674,17 @@ __global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __gri
   __shared__ __align__(16) float sq[4][D];
   __shared__ float part[4][32];
   const int kh = blockIdx.y, s = blockIdx.z;
+  const int seg = blockIdx.x % a.w_segs, tile0 = blockIdx.x / a.w_segs, tiles = gridDim.x / a.w_segs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const SeqSpan q = seq_span(a.c, a.ch, s);
   if (q.n <= 0) return;
   const int G = a.group;
   const int pre = min(a.prefix ? max(a.prefix[s], 0) : 0, q.kv);
   const ScoreMod sm = score_mod(a);
-  for (int tile = blockIdx.x; tile * 32 < q.kv; tile += gridDim.x) {
-    const int j0 = tile * 32, j1 = min(j0 + 32, q.kv);
+  for (int tile = tile0; tile * kWKeysF32 < q.kv; tile += tiles) {
+    const int j0 = tile * kWKeysF32, j1 = min(j0 + kWKeysF32, q.kv);
+    const bool cut = a.w_segs > 1 && j1 <= a.part_stride;
+    if (!cut && seg > 0) continue;
     __syncthreads();
     for (int i = tid; i < 32 * (D / 4); i += 128) {
       const int r = i / (D / 4), c = i % (D / 4);
@@ -621,8 +697,14 @@ __global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __gri
     const int j = j0 + lane;
     int t0 = max(0, j0 - q.old), t1 = min(q.n, j1 - 1 - q.old + min(a.window, kNoWindow - 1 - j1));
     if (j0 < pre) { t0 = 0; t1 = q.n; }
+    int ra = t0 * G, rz = max(t1 * G, ra);
+    if (cut) {
+      const int64_t all = rz - ra;
+      rz = ra + static_cast<int>(all * (seg + 1) / a.w_segs);
+      ra += static_cast<int>(all * seg / a.w_segs);
+    }
     float sum = 0.f;
-    for (int r = t0 * G + warp; r < t1 * G; r += 4) {
+    for (int r = ra + warp; r < rz; r += 4) {
       const int t = a.group_div.div(r), h = kh * G + r - t * G;
       const float* src = static_cast<const float*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head;
       __syncwarp();
@@ -642,15 +724,15 @@ __global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __gri
       const int i = q.old + t;
       const float z = a.lse[static_cast<int64_t>(q.row0 + t) * a.n_q_heads + h];
       const bool seen = z != -INFINITY && (j < pre || (j <= i && j > i - a.window));
-      const float v = score2(sm, dot, a.slopes ? a.slopes[h] * kLog2e : 0.f, abs(i - j));
+      const float v = score2(sm, dot, a.slopes ? a.slopes[h] * kLog2e : 0.f, i - j);
       sum += seen ? exp2f(v - z * kLog2e) : 0.f;
     }
     part[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && j < j1) {
-      const int64_t row = slot_row(a.c, s, kh, j);
       const float x = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
-      if (row >= 0) a.acc[row] = (a.acc_decay != 0.f ? a.acc_decay * a.acc[row] : 0.f) + x;
+      if (cut) weight_part(a, seg, s, kh)[j] = x;
+      else add_weight(a, slot_row(a.c, s, kh, j), x);
     }
   }
 }
@@ -671,9 +753,8 @@ cudaError_t launch_rows_d(const Launch& L, const PagedAttnArgs& a) {
 }
 
 template <int D, bool MOD>
-cudaError_t launch_weights(const Launch& L, const PagedAttnArgs& a, int64_t max_kv) {
+cudaError_t launch_weights(const Launch& L, const PagedAttnArgs& a, const dim3& grid) {
   constexpr size_t smem = (kWKeys + 2 * kWRows) * 2 * D + 3 * 2 * kWRows * 4;
-  const dim3 grid(static_cast<unsigned>((max_kv + kWKeys - 1) / kWKeys), a.c.n_heads, a.c.n_seqs);
   return launch_kernel(paged_attn_weights_kernel<D, MOD>, grid, dim3(128), smem, L.stream, a);
 }
 
@@ -702,14 +783,19 @@ cudaError_t launch_paged_attn_combine(const Launch& L, const PagedAttnArgs& a, b
 
 cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, bool bf16, int64_t max_kv) {
   const bool mod = a.cap > 0.f || a.slopes != nullptr;
-  if (!bf16) {
-    const dim3 grid(static_cast<unsigned>((max_kv + 31) / 32), a.c.n_heads, a.c.n_seqs);
-    return a.head_dim == 128 ? launch_kernel(paged_attn_weights_f32_kernel<128>, grid, dim3(128), 0, L.stream, a)
-                             : launch_kernel(paged_attn_weights_f32_kernel<64>, grid, dim3(128), 0, L.stream, a);
-  }
-  if (a.head_dim == 128)
-    return mod ? launch_weights<128, true>(L, a, max_kv) : launch_weights<128, false>(L, a, max_kv);
-  return mod ? launch_weights<64, true>(L, a, max_kv) : launch_weights<64, false>(L, a, max_kv);
+  const int keys = bf16 ? kWKeys : kWKeysF32;
+  const dim3 grid(static_cast<unsigned>((max_kv + keys - 1) / keys * a.w_segs), a.c.n_heads, a.c.n_seqs);
+  cudaError_t e;
+  if (!bf16)
+    e = a.head_dim == 128 ? launch_kernel(paged_attn_weights_f32_kernel<128>, grid, dim3(128), 0, L.stream, a)
+                          : launch_kernel(paged_attn_weights_f32_kernel<64>, grid, dim3(128), 0, L.stream, a);
+  else if (a.head_dim == 128)
+    e = mod ? launch_weights<128, true>(L, a, grid) : launch_weights<128, false>(L, a, grid);
+  else
+    e = mod ? launch_weights<64, true>(L, a, grid) : launch_weights<64, false>(L, a, grid);
+  if (e != cudaSuccess || a.w_segs == 1) return e;
+  const dim3 g(static_cast<unsigned>((max_kv + 127) / 128), a.c.n_heads, a.c.n_seqs);
+  return launch_kernel(paged_attn_weights_sum_kernel, g, dim3(128), 0, L.stream, a, keys);
 }
 
 }  // namespace vx

@@ -398,8 +398,19 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         }
         tmem_ld_wait();
         if constexpr (MOD) {
+          scale_scores(sm, sv);
+          if (sm.bias) {   // the list's gap, if the tile holds it: slots lie `shift` further behind key `gap`
+            const int gap = it.kl.cut - xt;
+            const float near = static_cast<float>(i - xt), far = static_cast<float>(i - xt - it.kl.shift);
+            if (gap <= 0 || gap >= kTcKeys) {
+              const float base = gap <= 0 ? far : near;
 #pragma unroll
-          for (int e = 0; e < 128; ++e) sv[e] = score2(sm, sv[e], slope2, abs(i - key_slot(it.kl, xt + e)));
+              for (int e = 0; e < 128; ++e) sv[e] = fmaf(-slope2, fabsf(base - e), sv[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 128; ++e) sv[e] = fmaf(-slope2, fabsf((e >= gap ? far : near) - e), sv[e]);
+            }
+          }
         }
         if (!((xt >= all_lo && xt + kTcKeys - 1 <= all_hi) || xt + kTcKeys - 1 < pre)) {
           const int lo = xlo - xt, hi = xhi - xt, pr = pre - xt;

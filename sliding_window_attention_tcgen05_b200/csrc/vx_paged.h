@@ -139,6 +139,9 @@ struct PagedAttnArgs {
   float cap;               // 0 = none
   float* acc;              // of the layer (track) or null
   float acc_decay;
+  int w_segs;              // segments of the rows in the sum of the weights
+  float* part_w;           // [w_segs][n_seqs][n_heads][part_stride] (w_segs > 1)
+  int64_t part_stride;     // slots
   int splits;              // parts of every sequence's key range
   float* part_o;           // [splits][n_tokens][n_q_heads][head_dim] (splits > 1)
   float2* part_ml;         // [splits][n_tokens][n_q_heads]: running max (log2) and sum
@@ -150,6 +153,7 @@ struct PagedAttnArgs {
 struct PagedAttnPlan {
   int kernel;    // 0: warp-level rows kernel, 1: tcgen05 kernel, 2: fp32 kernel
   int splits;
+  int w_segs;    // segments of the rows in the sum of the weights (track)
 };
 PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_heads, int group, int max_q,
                               int64_t max_kv);

@@ -399,6 +399,14 @@ def test_attention_layers_strides_and_repeats(dtype, news, D):
             assert torch.equal(got, b.acc[s][l].T)
 
 
+@pytest.mark.parametrize("dtype,kv", [(BF, 200), (F32, 77), (BF, 1 << 20)])
+def test_a_wrong_bound_on_the_lengths_costs_nothing_but_time(dtype, kv):
+    vx = _vx()
+    b = Batch([900, 45], [700, 300], 4, 2, 64, 16, dtype, weights=True)
+    o, lse = vx.paged_attn_fwd(b.cache, 0, b.q.cuda(), b.q_start, b.max_q, max_kv=kv, track=0.25, return_lse=True)
+    _check_attn(b, o, lse, track=0.25)
+
+
 @pytest.mark.parametrize("dtype,n,D", [(BF, 1, 64), (BF, 100, 64), (BF, 100, 128), (F32, 3, 64)])
 def test_queries_that_see_nothing(dtype, n, D):
     # Tokens past the table's slots have no key of their own; with a short window they see nothing at all.

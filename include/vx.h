@@ -353,7 +353,8 @@ VX_API size_t vx_stream_step_workspace(const vx_layer_cfg *cfg, int S, int n_new
  * [n_layers][n_pages][n_kv_heads][page_size] fp32.
  * All pointers are device pointers of the caller, who hands out the pages
  * (table entries of slots that no call touches may hold anything, -1 say).
- * head_dim 64 or 128, page_size 1 .. 65536, max_pages * page_size < 2^30.
+ * head_dim 64 or 128, page_size 1 .. 65536, max_pages * page_size < 2^30,
+ * n_pages * n_kv_heads * page_size < 2^31.
  *
  * A call processes a chunk of new tokens: sequence s owns the rows
  * q_start[s] .. q_start[s + 1] - 1 of the token tensors (device int32

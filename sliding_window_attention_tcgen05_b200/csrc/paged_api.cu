@@ -50,6 +50,9 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
   if (segs > most_segs) segs = most_segs;
   if (segs > 32) segs = 32;
   p.w_segs = static_cast<int>(segs < 1 ? 1 : segs);
+  // Up to 8 rows: their scores, 4 bytes a key each, against another read of K (2 * head_dim bytes a key); not where
+  // the tables' length would ask for a workspace of hundreds of megabytes.
+  p.keep_scores = p.kernel == 0 && rows <= 8 && lanes * rows * max_kv * 4 <= (256ll << 20);
   return p;
 }
 
@@ -75,6 +78,8 @@ vx_status check_cache(const vx_paged_cache* c, const char* what) {
   VX_CHECK_ARG(c->n_kv_heads >= 1 && c->n_kv_heads <= 1024, "%s: n_kv_heads must be 1 .. 1024", what);
   VX_CHECK_ARG(c->n_seqs >= 1 && c->n_seqs <= 65535, "%s: n_seqs must be 1 .. 65535", what);
   VX_CHECK_ARG(c->page_size >= 1 && c->page_size <= 65536, "%s: page_size must be 1 .. 65536", what);
+  VX_CHECK_ARG(static_cast<int64_t>(c->n_pages) * c->n_kv_heads * c->page_size < (1ll << 31),
+               "%s: n_pages * n_kv_heads * page_size must be below 2^31", what);
   VX_CHECK_ARG(c->max_pages >= 1 && static_cast<int64_t>(c->max_pages) * c->page_size < kMaxSlots,
                "%s: max_pages * page_size must be 1 .. 2^30 - 1", what);
   return VX_OK;
@@ -170,10 +175,13 @@ struct AttnCarve {
   float* part_o;
   float2* part_ml;
   float* part_w;
+  float* scores;
 };
-AttnCarve carve_attn(Carve& cv, const vx_paged_cache* c, int64_t n_tokens, int n_q_heads, const PagedAttnPlan& p,
-                     int64_t max_kv, bool lse, bool track) {
+int64_t score_stride(int64_t max_kv) { return (max_kv + 3) / 4 * 4; }
+AttnCarve carve_attn(Carve& cv, const vx_paged_cache* c, int64_t n_tokens, int n_q_heads, int max_q,
+                     const PagedAttnPlan& p, int64_t max_kv, bool lse, bool track) {
   AttnCarve r = {};
+  const int64_t rows_of_seq = static_cast<int64_t>(max_q) * (n_q_heads / c->n_kv_heads);
   const int64_t rows = n_tokens * n_q_heads;
   cv.take(kStatusBytes);
   if (track && !lse) r.lse = static_cast<float*>(cv.take(rows * 4));
@@ -181,7 +189,9 @@ AttnCarve carve_attn(Carve& cv, const vx_paged_cache* c, int64_t n_tokens, int n
     r.part_o = static_cast<float*>(cv.take(rows * p.splits * c->head_dim * 4));
     r.part_ml = static_cast<float2*>(cv.take(rows * p.splits * 8));
   }
-  if (track && p.w_segs > 1)
+  if (track && p.keep_scores)
+    r.scores = static_cast<float*>(cv.take(c->n_seqs * c->n_kv_heads * rows_of_seq * score_stride(max_kv) * 4));
+  else if (track && p.w_segs > 1)
     r.part_w = static_cast<float*>(cv.take(max_kv * p.w_segs * c->n_seqs * c->n_kv_heads * 4));
   return r;
 }
@@ -312,7 +322,7 @@ size_t vx_paged_attn_workspace(const vx_paged_cache* cache, int n_q_heads, int64
   const PagedAttnPlan p = plan_paged_attn(cache->dt == VX_BF16, cache->head_dim, cache->n_seqs, cache->n_kv_heads,
                                           group, mq, kv);
   Carve cv{nullptr, 0};
-  carve_attn(cv, cache, n_tokens, n_q_heads, p, kv, want_lse, track);
+  carve_attn(cv, cache, n_tokens, n_q_heads, mq, p, kv, want_lse, track);
   return align_up(cv.off, kAlign);
 }
 
@@ -343,10 +353,10 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
                what);
   const bool bf16 = cache->dt == VX_BF16;
   const int64_t kv = bound_kv(cache, max_kv);
-  PagedAttnPlan plan = {0, 1, 1};
+  PagedAttnPlan plan = {0, 1, 1, false};
   if (mq > 0) plan = plan_paged_attn(bf16, cache->head_dim, cache->n_seqs, cache->n_kv_heads, group, mq, kv);
   Carve cv{static_cast<uint8_t*>(ws), 0};
-  const AttnCarve bf = carve_attn(cv, cache, n_tokens, n_q_heads, plan, kv, lse != nullptr, track != 0);
+  const AttnCarve bf = carve_attn(cv, cache, n_tokens, n_q_heads, mq, plan, kv, lse != nullptr, track != 0);
   Launch L;
   if ((st = make_launch(&L, ws, ws_bytes, mq > 0 ? cv.off : kStatusBytes, stream)) != VX_OK) return st;
   if (mq == 0) return VX_OK;
@@ -381,6 +391,8 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
   a.w_segs = plan.w_segs;
   a.part_w = bf.part_w;
   a.part_stride = kv;
+  a.scores = bf.scores;
+  a.score_stride = score_stride(kv);
   a.status = L.status;
   a.limit_ns = L.limit_ns;
   const int64_t rows = static_cast<int64_t>(mq) * group;
@@ -394,7 +406,7 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
   if (plan.splits > 1)
     VX_CUDA(traced(L, "paged_attn_combine", 1, [&] { return launch_paged_attn_combine(L, a, bf16); }));
   if (track)
-    VX_CUDA(traced(L, "paged_attn_weights", plan.w_segs > 1 ? 2 : 1, [&] { return launch_paged_attn_weights(L, a, bf16, kv); }));
+    VX_CUDA(traced(L, "paged_attn_weights", plan.w_segs > 1 && !plan.keep_scores ? 2 : 1, [&] { return launch_paged_attn_weights(L, a, bf16, kv); }));
   return VX_OK;
 }
 

@@ -12,23 +12,29 @@ namespace {
 // paged_attn_rows_kernel: CTA per (key range, K/V head, sequence), four warps.
 // The up to 16 * MT query rows (token t, head g of the group: row t * G + g)
 // are the M side of mma.sync tiles, so one read of a K/V row serves the whole
-// group; tcgen05's M >= 64 tiles would be mostly padding.  Each warp walks its
-// own tiles of KT keys through its own ring of cp.async stages (no CTA barrier
-// in the loop), with the page of every row looked up one tile ahead; the four
-// warps' softmax states are joined through shared memory at the end.
+// group; tcgen05's M >= 64 tiles would be mostly padding.  With up to 8 rows
+// (HALF) the tile's lower half is left out of the softmax.  Each warp walks its
+// own tiles of KT keys through its own two cp.async stages (no CTA barrier in
+// the loop; three CTAs an SM are worth more than a third stage), with the page
+// of every row looked up one tile ahead; O is rescaled only when a row's
+// maximum grows by more than 2^8; the four warps' softmax states are joined
+// through shared memory at the end.
 constexpr int kRowsThreads = 128;
-constexpr int kRowsStages = 3;
+constexpr int kRowsStages = 2;
 constexpr int kRowsStageBytes = 8192;   // K and V of one warp tile
+constexpr float kRowsSlack = 8.0f;
 
-template <int D, int MT, bool MOD>
+template <int D, int MT, bool HALF, bool MOD>
 __global__ void __launch_bounds__(kRowsThreads)
 paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int KT = kRowsStageBytes / (4 * D);   // 16 keys (D 128) or 32 (D 64)
+  constexpr int NB = KT / 8;                      // 8-key blocks of a tile
+  constexpr int NH = HALF ? 1 : 2;                // 8-row halves of a 16-row tile in use
   constexpr int CPR = D / 8;                      // 16-byte chunks of a row
   constexpr int RPI = 32 / CPR;                   // rows per warp-wide copy
-  constexpr int ROWS = 16 * MT;
+  constexpr int ROWS = HALF ? 8 : 16 * MT;
   extern __shared__ __align__(128) uint8_t smem[];
   const int sp = blockIdx.x, kh = blockIdx.y, s = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -42,47 +48,51 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
   const int tiles = (x1 - x0 + KT - 1) / KT;
   const int mine = tiles > warp ? (tiles - warp + 3) / 4 : 0;
 
-  uint8_t* stage_base = smem + warp * kRowsStages * kRowsStageBytes;
-  const uint32_t stage_addr = smem_addr(stage_base);
-  const uint16_t* kp = static_cast<const uint16_t*>(a.k);
-  const uint16_t* vp = static_cast<const uint16_t*>(a.v);
+  const uint32_t stage_addr = smem_addr(smem) + warp * kRowsStages * kRowsStageBytes;
+  const int cc = lane % CPR, rl0 = lane / CPR;
+  const uint8_t* kp = static_cast<const uint8_t*>(a.k) + cc * 16;
+  const uint8_t* vp = static_cast<const uint8_t*>(a.v) + cc * 16;
 
-  const int lrow = lane & (KT - 1);
-  auto lookup = [&](int i) -> int64_t {   // this lane's row of the warp's tile i, or -1
-    const int x = x0 + (warp + 4 * i) * KT + lrow;
+  auto lookup = [&](int i) -> int {   // this lane's row of the warp's tile i, or -1
+    const int x = x0 + (warp + 4 * i) * KT + (lane & (KT - 1));
     if (i >= mine || x >= x1) return -1;
-    const int64_t r = slot_row(a.c, s, kh, key_slot(kl, x));
+    const int r = slot_row(a.c, s, kh, key_slot(kl, x));
     if (r < 0) report_bad_cache(a.status, s);
     return r;
   };
-  auto issue = [&](int i, int64_t row) {
+  auto issue = [&](int i, int row) {
     if (i < mine) {
-      const uint32_t st = stage_addr + (i % kRowsStages) * kRowsStageBytes;
+      const uint32_t dst = stage_addr + (i % kRowsStages) * kRowsStageBytes + rl0 * (2 * D);
+      int gr[KT / RPI];
+#pragma unroll
+      for (int it = 0; it < KT / RPI; ++it) gr[it] = __shfl_sync(0xffffffffu, row, it * RPI + rl0);
 #pragma unroll
       for (int it = 0; it < KT / RPI; ++it) {
-        const int r = it * RPI + lane / CPR, c = lane % CPR;
-        const int64_t gr = __shfl_sync(0xffffffffu, row, r);
-        const int64_t e = (gr < 0 ? 0 : gr) * D + c * 8;
-        const uint32_t dst = st + r * (2 * D) + ((c ^ (r & 7)) << 4);
-        cp_async16(dst, kp + e, gr >= 0);
-        cp_async16(dst + kRowsStageBytes / 2, vp + e, gr >= 0);
+        const int64_t off = static_cast<int64_t>(max(gr[it], 0)) * (2 * D);
+        const uint32_t d = dst + it * RPI * (2 * D) + ((cc ^ ((it * RPI + rl0) & 7)) << 4);
+        cp_async16(d, kp + off, gr[it] >= 0);
+        cp_async16(d + kRowsStageBytes / 2, vp + off, gr[it] >= 0);
       }
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < kRowsStages - 1; ++i) issue(i, lookup(i));
-  int64_t next_row = lookup(kRowsStages - 1);
+  issue(0, lookup(0));
+  int next_row = lookup(1);
 
   // Query fragments (A operand) and each row's place: rows lane / 4 and + 8 of every 16-row tile.
   const int qr = lane >> 2, qc = (lane & 3) * 2;
   uint32_t qa[MT][D / 16][4];
-  int xlo[MT][2], xhi[MT][2], qi[MT][2];
-  float slope2[MT][2];
+  int xlo[MT][NH], xhi[MT][NH], qi[MT][NH];
+  float slope2[MT][NH];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
+      if (half >= NH) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) qa[mt][ks][1] = qa[mt][ks][3] = 0u;
+        continue;
+      }
       const int r = mt * 16 + half * 8 + qr;
       const bool ok = r < rows;
       const int t = a.group_div.div(ok ? r : 0), g = (ok ? r : 0) - t * G;
@@ -99,110 +109,142 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
       }
     }
   const ScoreMod sm = score_mod(a);
+  const float sc = MOD ? 1.f : sm.sl2;
   const int pre = min(kl.pre, x1);
   // Tiles inside [all_lo, all_hi] or below pre need no mask.
   const int all_lo = max(0, q.old + q.n - 1 - a.window + 1 - kl.shift), all_hi = min(q.old - kl.shift, x1 - 1);
+  // Scores kept for the sum of the weights: this lane's row of them.
+  float* kept = nullptr;
+  if (HALF && a.scores != nullptr && qr < rows)
+    kept = a.scores + ((static_cast<int64_t>(s) * a.c.n_heads + kh) * (a.ch.max_q * G) + qr) * a.score_stride;
 
   float o[MT][D / 8][4];
-  float m_run[MT][2], l_part[MT][2];
+  float m_run[MT][NH], l_part[MT][NH];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    m_run[mt][0] = m_run[mt][1] = -INFINITY;
-    l_part[mt][0] = l_part[mt][1] = 0.f;
+#pragma unroll
+    for (int half = 0; half < NH; ++half) {
+      m_run[mt][half] = -INFINITY;
+      l_part[mt][half] = 0.f;
+    }
 #pragma unroll
     for (int nb = 0; nb < D / 8; ++nb) o[mt][nb][0] = o[mt][nb][1] = o[mt][nb][2] = o[mt][nb][3] = 0.f;
   }
 
   for (int i = 0; i < mine; ++i) {
-    cp_async_wait<kRowsStages - 2>();
+    cp_async_wait<0>();
     __syncwarp();
-    {   // the stage read in the last turn is free again
-      const int64_t row = next_row;
-      next_row = lookup(i + kRowsStages);
-      issue(i + kRowsStages - 1, row);
-    }
+    issue(i + 1, next_row);   // into the stage read in the last turn
+    next_row = lookup(i + 2);
     const uint32_t kb = stage_addr + (i % kRowsStages) * kRowsStageBytes, vb = kb + kRowsStageBytes / 2;
-    const int xt = x0 + (warp + 4 * i) * KT;
+    const int xb = x0 + (warp + 4 * i) * KT;
+    float sa[MT][NB][4];
 #pragma unroll
-    for (int b = 0; b < KT / 16; ++b) {
-      const int xb = xt + b * 16;
-      if (xb >= x1) break;
-      float sa[MT][2][4];
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
+      for (int mt = 0; mt < MT; ++mt) sa[mt][nb][0] = sa[mt][nb][1] = sa[mt][nb][2] = sa[mt][nb][3] = 0.f;
+      const int kr = nb * 8 + (lane & 7);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) sa[mt][nb][0] = sa[mt][nb][1] = sa[mt][nb][2] = sa[mt][nb][3] = 0.f;
-        const int kr = b * 16 + nb * 8 + (lane & 7);
+      for (int h = 0; h < D / 32; ++h) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(kb + kr * (2 * D) + (((h * 4 + (lane >> 3)) ^ (kr & 7)) << 4), b0, b1, b2, b3);
 #pragma unroll
-        for (int h = 0; h < D / 32; ++h) {
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4(kb + kr * (2 * D) + (((h * 4 + (lane >> 3)) ^ (kr & 7)) << 4), b0, b1, b2, b3);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_bf16_16816(sa[mt][nb], qa[mt][2 * h][0], qa[mt][2 * h][1], qa[mt][2 * h][2], qa[mt][2 * h][3], b0, b1);
-            mma_bf16_16816(sa[mt][nb], qa[mt][2 * h + 1][0], qa[mt][2 * h + 1][1], qa[mt][2 * h + 1][2],
-                           qa[mt][2 * h + 1][3], b2, b3);
-          }
+        for (int mt = 0; mt < MT; ++mt) {
+          mma_bf16_16816(sa[mt][nb], qa[mt][2 * h][0], qa[mt][2 * h][1], qa[mt][2 * h][2], qa[mt][2 * h][3], b0, b1);
+          mma_bf16_16816(sa[mt][nb], qa[mt][2 * h + 1][0], qa[mt][2 * h + 1][1], qa[mt][2 * h + 1][2],
+                         qa[mt][2 * h + 1][3], b2, b3);
         }
       }
-      const bool clean = (xb >= all_lo && xb + 15 <= all_hi) || xb + 15 < pre;
-      uint32_t pa[MT][4];
-      bool grew = false;
-      float alpha[MT][2];
+    }
+    const bool clean = (xb >= all_lo && xb + KT - 1 <= all_hi) || xb + KT - 1 < pre;
+    uint32_t pa[MT][KT / 16][4];
+    bool grew = false;
+    float alpha[MT][NH];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (half >= NH) {
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k) pa[mt][k][1] = pa[mt][k][3] = 0u;
+          continue;
+        }
+        float y[2 * NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          y[2 * nb] = sa[mt][nb][2 * half];
+          y[2 * nb + 1] = sa[mt][nb][2 * half + 1];
+        }
+        if constexpr (MOD) {
+          scale_scores(sm, y);
+          if (sm.bias)
+#pragma unroll
+            for (int e = 0; e < 2 * NB; ++e) {
+              const int j = key_slot(kl, xb + (e >> 1) * 8 + qc + (e & 1));
+              y[e] -= slope2[mt][half] * static_cast<float>(abs(qi[mt][half] - j));
+            }
+        }
+        if (!clean) {
+#pragma unroll
+          for (int e = 0; e < 2 * NB; ++e) {
+            const int x = xb + (e >> 1) * 8 + qc + (e & 1);
+            y[e] = (x < pre || (x >= xlo[mt][half] && x <= xhi[mt][half] && x < x1)) ? y[e] : -INFINITY;
+          }
+        }
+        if (HALF && kept != nullptr) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int x = xb + nb * 8 + qc;
+            if (x < a.score_stride) *reinterpret_cast<float2*>(kept + x) = make_float2(y[2 * nb] * sc, y[2 * nb + 1] * sc);
+          }
+        }
+        float cmax = fmaxf(y[0], y[1]);
+#pragma unroll
+        for (int e = 2; e < 2 * NB; e += 2) cmax = fmaxf(cmax, fmaxf(y[e], y[e + 1]));
+        cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, 1));
+        cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, 2)) * sc;
+        alpha[mt][half] = 1.f;
+        if (cmax > m_run[mt][half] + kRowsSlack) {
+          alpha[mt][half] = ex2_approx(m_run[mt][half] - cmax);   // 0 for the first keys
+          m_run[mt][half] = cmax;
+          grew = true;
+        }
+        const float mu = m_run[mt][half] == -INFINITY ? 0.f : m_run[mt][half];
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2 * NB; ++e) {
+          y[e] = ex2_approx(fmaf(y[e], sc, -mu));
+          sum += y[e];
+        }
+        l_part[mt][half] = l_part[mt][half] * alpha[mt][half] + sum;
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k) {
+          pa[mt][k][half] = pack_bf16x2(y[4 * k], y[4 * k + 1]);
+          pa[mt][k][half + 2] = pack_bf16x2(y[4 * k + 2], y[4 * k + 3]);
+        }
+      }
+    if (__any_sync(0xffffffffu, grew)) {   // alpha is 1 for every row otherwise
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float cmax = -INFINITY;
-          float y[4] = {sa[mt][0][2 * half], sa[mt][0][2 * half + 1], sa[mt][1][2 * half], sa[mt][1][2 * half + 1]};
-          if constexpr (MOD) scale_scores(sm, y);
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& v = sa[mt][nb][2 * half + e];
-              const int x = xb + nb * 8 + qc + e;
-              v = MOD ? y[2 * nb + e] : v * sm.sl2;
-              if (MOD && sm.bias) v -= slope2[mt][half] * static_cast<float>(abs(qi[mt][half] - key_slot(kl, x)));
-              if (!clean) v = (x < pre || (x >= xlo[mt][half] && x <= xhi[mt][half] && x < x1)) ? v : -INFINITY;
-              cmax = fmaxf(cmax, v);
-            }
-          cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, 1));
-          cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, 2));
-          const float m_new = fmaxf(m_run[mt][half], cmax);
-          const float mu = m_new == -INFINITY ? 0.f : m_new;
-          alpha[mt][half] = ex2_approx(m_run[mt][half] - mu);
-          grew |= m_new != m_run[mt][half];
-          m_run[mt][half] = m_new;
-          float p[2][2];
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) p[nb][e] = ex2_approx(sa[mt][nb][2 * half + e] - mu);
-          l_part[mt][half] = l_part[mt][half] * alpha[mt][half] + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
-          pa[mt][half] = pack_bf16x2(p[0][0], p[0][1]);
-          pa[mt][half + 2] = pack_bf16x2(p[1][0], p[1][1]);
+        for (int nb = 0; nb < D / 8; ++nb) {
+          o[mt][nb][0] *= alpha[mt][0];
+          o[mt][nb][1] *= alpha[mt][0];
+          o[mt][nb][2] *= alpha[mt][NH - 1];
+          o[mt][nb][3] *= alpha[mt][NH - 1];
         }
-      if (__any_sync(0xffffffffu, grew)) {   // alpha is 1 for every row otherwise
+    }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int nb = 0; nb < D / 8; ++nb) {
-            o[mt][nb][0] *= alpha[mt][0];
-            o[mt][nb][1] *= alpha[mt][0];
-            o[mt][nb][2] *= alpha[mt][1];
-            o[mt][nb][3] *= alpha[mt][1];
-          }
-      }
-      const int vr = b * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+    for (int k = 0; k < KT / 16; ++k) {
+      const int vr = k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
       for (int dc = 0; dc < D / 8; dc += 2) {
         uint32_t b0, b1, b2, b3;
         ldsm_x4_t(vb + vr * (2 * D) + (((dc + (lane >> 4)) ^ (vr & 7)) << 4), b0, b1, b2, b3);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          mma_bf16_16816(o[mt][dc], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b0, b1);
-          mma_bf16_16816(o[mt][dc + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b2, b3);
+          mma_bf16_16816(o[mt][dc], pa[mt][k][0], pa[mt][k][1], pa[mt][k][2], pa[mt][k][3], b0, b1);
+          mma_bf16_16816(o[mt][dc + 1], pa[mt][k][0], pa[mt][k][1], pa[mt][k][2], pa[mt][k][3], b2, b3);
         }
       }
     }
@@ -217,7 +259,7 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < NH; ++half) {
       float l = l_part[mt][half];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -325,10 +367,10 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
       const int r = i / (D / 4), c = i % (D / 4);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       if (xt + r < x1) {
-        const int64_t gr = slot_row(a.c, s, kh, key_slot(kl, xt + r));
+        const int gr = slot_row(a.c, s, kh, key_slot(kl, xt + r));
         if (gr >= 0) {
-          x = *reinterpret_cast<const float4*>(kp + gr * D + c * 4);
-          y = *reinterpret_cast<const float4*>(vp + gr * D + c * 4);
+          x = *reinterpret_cast<const float4*>(kp + static_cast<int64_t>(gr) * D + c * 4);
+          y = *reinterpret_cast<const float4*>(vp + static_cast<int64_t>(gr) * D + c * 4);
         } else {
           report_bad_cache(a.status, s);
         }
@@ -408,60 +450,85 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------- combine --
-// One warp per (token, head): the parts' maxima and sums, then the weighted
-// sum of their outputs, D / 32 elements per lane.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+// W warps per (token, head): the parts' maxima and sums, then the weighted sum
+// of their outputs, D / 32 elements per lane, the parts dealt to the warps and
+// all of a warp's loads in flight together; the warps' sums are added in order.
+constexpr int kCombineThreads = 256;
+constexpr int kCombineDeep = 8;   // loads in flight
+
+template <int D, bool BF16, int W>
+__global__ void __launch_bounds__(kCombineThreads) paged_attn_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int V = D / 32, RB = kCombineThreads / 32 / W;   // rows of a block
+  __shared__ float part[RB][W][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp / W, w = warp % W;
   const int64_t rows = static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= rows) return;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * RB + rb;
   const int64_t tok = row / a.n_q_heads;
   const int h = static_cast<int>(row - tok * a.n_q_heads);
-  // Rows outside every sequence (or past max_q) have no parts: find the row's sequence.
-  int lo = 0, hi = a.c.n_seqs;   // last s with q_start[s] <= tok
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.ch.q_start[mid] <= tok) lo = mid; else hi = mid;
+  bool mine = row < rows;
+  if (mine) {
+    // Rows outside every sequence (or past max_q) have no parts: find the row's sequence.
+    int lo = 0, hi = a.c.n_seqs;   // last s with q_start[s] <= tok
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.ch.q_start[mid] <= tok) lo = mid; else hi = mid;
+    }
+    const SeqSpan q = seq_span(a.c, a.ch, lo);
+    mine = tok >= q.row0 && tok < q.row0 + q.n;
   }
-  const SeqSpan q = seq_span(a.c, a.ch, lo);
-  if (tok < q.row0 || tok >= q.row0 + q.n) return;
-  float2 ml[kMaxSplits / 32];
-  float M = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kMaxSplits / 32; ++i) {
-    const int sp = i * 32 + lane;
-    ml[i] = sp < a.splits ? a.part_ml[sp * rows + row] : make_float2(-INFINITY, 0.f);
-    M = fmaxf(M, ml[i].x);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float l = 0.f, w[kMaxSplits / 32];
-#pragma unroll
-  for (int i = 0; i < kMaxSplits / 32; ++i) {
-    w[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - M);
-    l += ml[i].y * w[i];
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  float y[V];
+  float M = -INFINITY, l = 0.f, y[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) y[e] = 0.f;
+  if (mine) {
+    float2 ml[kMaxSplits / 32];
 #pragma unroll
-  for (int i = 0; i < kMaxSplits / 32; ++i)
-#pragma unroll 4
-    for (int j = 0; j < 32; ++j) {
-      const int sp = i * 32 + j;
-      if (sp >= a.splits) break;
-      const float ws = __shfl_sync(0xffffffffu, w[i], j);
-      if (ws == 0.f) continue;   // an empty part wrote no output
-      const float* src = a.part_o + (sp * rows + row) * D + lane * V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = fmaf(src[e], ws, y[e]);
+    for (int i = 0; i < kMaxSplits / 32; ++i) {
+      const int sp = i * 32 + lane;
+      ml[i] = sp < a.splits ? a.part_ml[sp * rows + row] : make_float2(-INFINITY, 0.f);
+      M = fmaxf(M, ml[i].x);
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float wt[kMaxSplits / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 32; ++i) {
+      wt[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - M);
+      l += ml[i].y * wt[i];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 32; ++i)
+      for (int j0 = w; j0 < 32 && i * 32 + j0 < a.splits; j0 += W * kCombineDeep) {
+        float x[kCombineDeep][V], ws[kCombineDeep];
+#pragma unroll
+        for (int k = 0; k < kCombineDeep; ++k) {
+          const int j = j0 + k * W, sp = i * 32 + j;
+          ws[k] = __shfl_sync(0xffffffffu, wt[i], j & 31);
+          if (j >= 32 || sp >= a.splits) ws[k] = 0.f;
+          const float* src = a.part_o + (sp * rows + row) * D + lane * V;
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[k][e] = ws[k] == 0.f ? 0.f : src[e];   // an empty part wrote no output
+        }
+#pragma unroll
+        for (int k = 0; k < kCombineDeep; ++k)
+#pragma unroll
+          for (int e = 0; e < V; ++e) y[e] = fmaf(x[k][e], ws[k], y[e]);
+      }
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) part[rb][w][lane * V + e] = y[e];
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int k = 1; k < W; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] += part[rb][k][lane * V + e];
+  }
+  if (!mine) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   if constexpr (BF16) {
     uint16_t* dst = static_cast<uint16_t*>(a.o) + tok * a.o_row + h * a.o_head + lane * V;
@@ -556,8 +623,8 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
     if (blocks > 0) {
       for (int i = tid; i < kWKeys * CPR; i += 128) {
         const int r = i / CPR, c = i % CPR;
-        const int64_t gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
-        cp_async16(sk + r * 2 * D + ((c ^ (r & 7)) << 4), kp + (gr < 0 ? 0 : gr) * D + c * 8, gr >= 0);
+        const int gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
+        cp_async16(sk + r * 2 * D + ((c ^ (r & 7)) << 4), kp + static_cast<int64_t>(max(gr, 0)) * D + c * 8, gr >= 0);
       }
       stage_q(0, 0);
     }
@@ -647,6 +714,50 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
   }
 }
 
+// The same sum from the scores that the rows kernel kept (base 2, by list
+// position; up to 8 rows, so that writing and reading them costs less than
+// reading K again).  A thread per slot.
+template <int D>
+__global__ void __launch_bounds__(256) paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s_lse[8];
+  const int kh = blockIdx.y, s = blockIdx.z;
+  const SeqSpan q = seq_span(a.c, a.ch, s);
+  if (q.n <= 0) return;
+  const int G = a.group, rows = q.n * G, cap = a.ch.max_q * G;
+  if (threadIdx.x < rows) {
+    const int t = a.group_div.div(threadIdx.x), h = kh * G + threadIdx.x - t * G;
+    const float z = a.lse[static_cast<int64_t>(q.row0 + t) * a.n_q_heads + h];
+    s_lse[threadIdx.x] = z == -INFINITY ? INFINITY : z * kLog2e;   // weight 0 without a sum
+  }
+  __syncthreads();
+  const KeyList kl = key_list(q.old, q.old + q.n - 1, a.window, a.prefix ? a.prefix[s] : 0, q.kv);
+  const float* kept = a.scores + (static_cast<int64_t>(s) * a.c.n_heads + kh) * cap * a.score_stride;
+  for (int j = blockIdx.x * 256 + threadIdx.x; j < q.kv; j += gridDim.x * 256) {
+    const int x = j < kl.cut ? j : j - kl.shift;
+    const int row = slot_row(a.c, s, kh, j);
+    float sum = 0.f;
+    if (x >= (j < kl.cut ? 0 : kl.cut) && x < kl.total) {
+      if (x < a.score_stride) {
+        for (int r = 0; r < rows; ++r) sum += ex2_approx(kept[r * a.score_stride + x] - s_lse[r]);
+      } else if (row >= 0) {   // the caller's max_kv was too low: the product again
+        const ScoreMod sm = score_mod(a);
+        const uint16_t* k = static_cast<const uint16_t*>(a.k) + static_cast<int64_t>(row) * D;
+        for (int r = 0; r < rows; ++r) {
+          const int t = a.group_div.div(r), h = kh * G + r - t * G, i = q.old + t;
+          if (!(j < kl.pre || (j <= i && j > i - a.window))) continue;
+          const uint16_t* qp = static_cast<const uint16_t*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head;
+          float dot = 0.f;
+          for (int d = 0; d < D; ++d) dot = fmaf(bf16_to_f(qp[d]), bf16_to_f(k[d]), dot);
+          sum += ex2_approx(score2(sm, dot, a.slopes ? a.slopes[h] * kLog2e : 0.f, i - j) - s_lse[r]);
+        }
+      }
+    }
+    add_weight(a, row, sum);
+  }
+}
+
 // Adds up the segments' sums.
 __global__ void __launch_bounds__(128) paged_attn_weights_sum_kernel(const __grid_constant__ PagedAttnArgs a, int keys) {
   pdl_wait();
@@ -688,9 +799,9 @@ __global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __gri
     __syncthreads();
     for (int i = tid; i < 32 * (D / 4); i += 128) {
       const int r = i / (D / 4), c = i % (D / 4);
-      const int64_t gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
+      const int gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
       *reinterpret_cast<float4*>(&sk[r][c * 4]) =
-          gr >= 0 ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + gr * D + c * 4)
+          gr >= 0 ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + static_cast<int64_t>(gr) * D + c * 4)
                   : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __syncthreads();
@@ -737,19 +848,32 @@ __global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __gri
   }
 }
 
-template <int D, int MT, bool MOD>
+template <int D, int MT, bool HALF, bool MOD>
 cudaError_t launch_rows(const Launch& L, const PagedAttnArgs& a) {
   constexpr size_t ring = 4 * kRowsStages * kRowsStageBytes;
-  constexpr size_t join = (2 * 4 * 16 * MT + 4 * 16 * MT * D) * sizeof(float);
+  constexpr size_t rows = HALF ? 8 : 16 * MT;
+  constexpr size_t join = (2 * 4 * rows + 4 * rows * D) * sizeof(float);
   constexpr size_t smem = ring > join ? ring : join;
   const dim3 grid(a.splits, a.c.n_heads, a.c.n_seqs);
-  return launch_kernel(paged_attn_rows_kernel<D, MT, MOD>, grid, dim3(kRowsThreads), smem, L.stream, a);
+  return launch_kernel(paged_attn_rows_kernel<D, MT, HALF, MOD>, grid, dim3(kRowsThreads), smem, L.stream, a);
 }
-template <int D>
+template <int D, bool MOD>
 cudaError_t launch_rows_d(const Launch& L, const PagedAttnArgs& a) {
-  const bool mod = a.cap > 0.f || a.slopes != nullptr;
-  if (a.ch.max_q * a.group <= 16) return mod ? launch_rows<D, 1, true>(L, a) : launch_rows<D, 1, false>(L, a);
-  return mod ? launch_rows<D, 2, true>(L, a) : launch_rows<D, 2, false>(L, a);
+  const int rows = a.ch.max_q * a.group;
+  return rows <= 8    ? launch_rows<D, 1, true, MOD>(L, a)
+         : rows <= 16 ? launch_rows<D, 1, false, MOD>(L, a)
+                      : launch_rows<D, 2, false, MOD>(L, a);
+}
+
+// Few rows get eight warps each, so that their parts are read by several SMs' worth of loads at once.
+template <int D, bool BF16>
+cudaError_t launch_combine(const Launch& L, const PagedAttnArgs& a) {
+  const int64_t rows = static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
+  const dim3 block(kCombineThreads);
+  if (rows <= 8 * L.sm_count && a.splits >= 16)
+    return launch_kernel(paged_attn_combine_kernel<D, BF16, 8>, dim3(static_cast<unsigned>(rows)), block, 0, L.stream, a);
+  return launch_kernel(paged_attn_combine_kernel<D, BF16, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), block, 0,
+                       L.stream, a);
 }
 
 template <int D, bool MOD>
@@ -761,7 +885,9 @@ cudaError_t launch_weights(const Launch& L, const PagedAttnArgs& a, const dim3& 
 }  // namespace
 
 cudaError_t launch_paged_attn_rows(const Launch& L, const PagedAttnArgs& a) {
-  return a.head_dim == 128 ? launch_rows_d<128>(L, a) : launch_rows_d<64>(L, a);
+  const bool mod = a.cap > 0.f || a.slopes != nullptr;
+  if (a.head_dim == 128) return mod ? launch_rows_d<128, true>(L, a) : launch_rows_d<128, false>(L, a);
+  return mod ? launch_rows_d<64, true>(L, a) : launch_rows_d<64, false>(L, a);
 }
 
 cudaError_t launch_paged_attn_f32(const Launch& L, const PagedAttnArgs& a) {
@@ -772,17 +898,17 @@ cudaError_t launch_paged_attn_f32(const Launch& L, const PagedAttnArgs& a) {
 }
 
 cudaError_t launch_paged_attn_combine(const Launch& L, const PagedAttnArgs& a, bool bf16) {
-  const int64_t rows = static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4)), block(128);
-  if (a.head_dim == 128)
-    return bf16 ? launch_kernel(paged_attn_combine_kernel<128, true>, grid, block, 0, L.stream, a)
-                : launch_kernel(paged_attn_combine_kernel<128, false>, grid, block, 0, L.stream, a);
-  return bf16 ? launch_kernel(paged_attn_combine_kernel<64, true>, grid, block, 0, L.stream, a)
-              : launch_kernel(paged_attn_combine_kernel<64, false>, grid, block, 0, L.stream, a);
+  if (a.head_dim == 128) return bf16 ? launch_combine<128, true>(L, a) : launch_combine<128, false>(L, a);
+  return bf16 ? launch_combine<64, true>(L, a) : launch_combine<64, false>(L, a);
 }
 
 cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, bool bf16, int64_t max_kv) {
   const bool mod = a.cap > 0.f || a.slopes != nullptr;
+  if (a.scores != nullptr) {
+    const dim3 g(static_cast<unsigned>((max_kv + 255) / 256), a.c.n_heads, a.c.n_seqs);
+    return a.head_dim == 128 ? launch_kernel(paged_attn_weights_kept_kernel<128>, g, dim3(256), 0, L.stream, a)
+                             : launch_kernel(paged_attn_weights_kept_kernel<64>, g, dim3(256), 0, L.stream, a);
+  }
   const int keys = bf16 ? kWKeys : kWKeysF32;
   const dim3 grid(static_cast<unsigned>((max_kv + keys - 1) / keys * a.w_segs), a.c.n_heads, a.c.n_seqs);
   cudaError_t e;

@@ -192,7 +192,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         }
       }
       cp_async_commit();
-      // Pool rows of four rows of tile u, or -1 (below 2^31, checked at launch): lane * 4 + k where runs are fetched
+      // Pool rows of four rows of tile u, or -1: lane * 4 + k where runs are fetched
       // by TMA (so that a run's rows are R / 4 neighbouring lanes'), else lane + 32 k.
       const bool tma = run >= 16;
       auto lookup = [&](int u, int (&row)[4]) {
@@ -203,7 +203,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           if (u >= it.nt || x >= it.x1) continue;
           const int j = key_slot(it.kl, x);
           if (!wanted(it.kl, j)) continue;
-          row[k] = static_cast<int>(slot_row(a.c, it.s, it.kh, j));
+          row[k] = slot_row(a.c, it.s, it.kh, j);
           if (row[k] < 0) report_bad_cache(a.status, it.s);
         }
       };
@@ -531,7 +531,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 template <int D, bool MOD>
 cudaError_t launch_tc(const Launch& L, const PagedAttnArgs& a, int blocks) {
   const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) * a.c.n_heads * a.c.page.d;
-  if (rows >= 1ull << 31) return cudaErrorInvalidValue;   // a row's number is a 32-bit coordinate (256 GB of K at D = 64)
   CUtensorMap tk, tv;
   const uint64_t dims[2] = {D, rows}, strides[1] = {D * 2};
   // Runs: the largest power of two that divides the page size, up to a tile.  Below 16 rows a TMA copy each costs more

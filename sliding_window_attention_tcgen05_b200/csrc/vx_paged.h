@@ -64,12 +64,13 @@ __device__ __forceinline__ void report_bad_cache(DevStatus* st, int s) {
 
 // Row index ((page, head, row) flattened, in units of one head's row) of slot
 // j, or -1 when the table's entry is not a page of the pool.  j must lie below
-// max_pages * page size.
-__device__ __forceinline__ int64_t slot_row(const PagedView& c, int s, int head, int j) {
+// max_pages * page size; a layer's pool has fewer than 2^31 rows.
+__device__ __forceinline__ int slot_row(const PagedView& c, int s, int head, int j) {
   const uint32_t pg = c.page.div(static_cast<uint32_t>(j));
   const int id = c.table[static_cast<int64_t>(s) * c.max_pages + pg];
   if (id < 0 || id >= c.n_pages) return -1;
-  return (static_cast<int64_t>(id) * c.n_heads + head) * c.page.d + (j - static_cast<int>(pg * c.page.d));
+  const int page = static_cast<int>(c.page.d);
+  return (id * c.n_heads + head) * page + (j - static_cast<int>(pg) * page);
 }
 
 // ---------------------------------------------------------------- rotary --
@@ -140,6 +141,8 @@ struct PagedAttnArgs {
   float* acc;              // of the layer (track) or null
   float acc_decay;
   int w_segs;              // segments of the rows in the sum of the weights
+  float* scores;           // [n_seqs][n_heads][max_q * group][score_stride] (plan's keep_scores) or null
+  int64_t score_stride;    // of list positions, a multiple of 4
   float* part_w;           // [w_segs][n_seqs][n_heads][part_stride] (w_segs > 1)
   int64_t part_stride;     // slots
   int splits;              // parts of every sequence's key range
@@ -154,6 +157,7 @@ struct PagedAttnPlan {
   int kernel;    // 0: warp-level rows kernel, 1: tcgen05 kernel, 2: fp32 kernel
   int splits;
   int w_segs;    // segments of the rows in the sum of the weights (track)
+  bool keep_scores;   // the rows kernel leaves its scores for the sum of the weights (track)
 };
 PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_heads, int group, int max_q,
                               int64_t max_kv);

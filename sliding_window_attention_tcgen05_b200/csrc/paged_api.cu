@@ -3,6 +3,7 @@
 // the key split, workspace carving.
 #include <cmath>
 #include <climits>
+#include <cstring>
 
 #include "vx_api.h"
 #include "paged_attn.cuh"
@@ -30,7 +31,7 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
     // A row block of the tcgen05 kernel would be at least three quarters padding.
     p.kernel = 0;
     ctas = lanes;
-    want = 8 * kPlanSms;
+    want = 12 * kPlanSms;
     min_keys = 256;
   } else {
     p.kernel = 1;
@@ -137,6 +138,18 @@ vx_status rope_table(const vx_rope_cfg* r, int head_dim, RopeTable* t, const cha
   VX_CHECK_ARG(!yarn || (r->orig_len >= 1 && std::isfinite(r->beta_fast) && std::isfinite(r->beta_slow) &&
                          r->beta_fast > r->beta_slow && std::isfinite(r->mscale) && r->mscale >= 0.0),
                "%s: yarn needs orig_len >= 1, beta_fast > beta_slow and mscale >= 0", what);
+  // The thread's last table: a model's calls all ask for the same one.
+  struct Last {
+    vx_rope_cfg cfg;   // no padding: compared as bytes
+    int head_dim;
+    RopeTable t;
+  };
+  static_assert(sizeof(vx_rope_cfg) == 4 * sizeof(int) + 5 * sizeof(double), "vx_rope_cfg has padding");
+  static thread_local Last last = {};   // head_dim 0: none yet
+  if (last.head_dim == head_dim && std::memcmp(&last.cfg, r, sizeof(*r)) == 0) {
+    *t = last.t;
+    return VX_OK;
+  }
   long double theta = r->theta;
   if (r->scaling == VX_ROPE_NTK) theta *= powl(r->factor, static_cast<long double>(rot) / (rot - 2));
   const long double two_pi = 6.283185307179586476925286766559L;
@@ -161,6 +174,9 @@ vx_status rope_table(const vx_rope_cfg* r, int head_dim, RopeTable* t, const cha
   t->mscale = yarn ? static_cast<float>(r->mscale > 0.0 ? r->mscale : 0.1 * std::log(r->factor) + 1.0) : 1.f;
   t->pairs = rot / 2;
   t->interleaved = r->interleaved != 0;
+  last.cfg = *r;
+  last.head_dim = head_dim;
+  last.t = *t;
   return VX_OK;
 }
 

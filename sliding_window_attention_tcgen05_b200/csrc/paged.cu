@@ -268,24 +268,40 @@ __device__ __forceinline__ int64_t evict_len(const EvictArgs& a, int s, bool* ba
   return len < 0 ? 0 : len < cap ? len : cap;
 }
 
-// CTA per (head, sequence, layer): the bar (the (m - r)-th largest key among
-// the first n = L - r slots) by a radix selection of 8-bit digits, from keys
-// read once into shared memory (when they fit), then the kept slots in slot
-// order, with the bar's equals taken from the lowest slot.  The histogram has
-// kSelCopies copies, one per lane modulo kSelCopies, because weights crowd
-// into few bins; the selection stops as soon as a whole bin is wanted.
+// Cluster of C CTAs per (head, sequence, layer): the bar (the (m - r)-th
+// largest key among the first n = L - r slots) by a radix selection of 8-bit
+// digits, from keys read once into shared memory (when they fit), then the
+// kept slots in slot order, with the bar's equals taken from the lowest slot.
+// Each CTA owns a run of slots and each of its warps a run of those; the CTAs
+// read one another's digit counts through distributed shared memory and all
+// come to the same bar (4 sequences of 32768 slots, 8 heads: 49 us with one
+// CTA each).  The histogram has kSelCopies copies, one per lane modulo
+// kSelCopies, because weights crowd into few bins; the selection stops as soon
+// as a whole bin is wanted.
 constexpr int kSelCopies = 8;
 
-template <int T>
-__global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__ EvictArgs a, int max_keys) {
+// The same shared-memory word of the cluster's CTA `rank`.
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_cta(smem_addr(p), rank)) : "memory");
+  return v;
+}
+
+template <int T, int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(T)
+evict_select_kernel(const __grid_constant__ EvictArgs a, int max_keys) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ uint32_t keys[];                 // max_keys
+  extern __shared__ uint32_t keys[];                 // max_keys, of this CTA's run
   __shared__ int hist[kSelCopies][257];
+  __shared__ int counts[2][256];                     // of this CTA: read by the others, in alternate passes
   __shared__ int s_digit, s_rest, s_whole;
-  __shared__ int wsum[2][32];
-  const int h = blockIdx.x, s = blockIdx.y, l = blockIdx.z;
+  __shared__ int wsum[2][32], s_cta[2];
+  const int h = blockIdx.x / C, c = blockIdx.x % C, s = blockIdx.y, l = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto cluster_sync = [&] {
+    if constexpr (C > 1) cluster_sync_all(); else __syncthreads();
+  };
   bool bad;
   const int L = static_cast<int>(evict_len(a, s, &bad));
   if (bad && tid == 0) report_bad_cache(a.status, s);
@@ -293,39 +309,49 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
   const int r = static_cast<int>(a.recent < m ? a.recent : m);
   const int n = L - r, want = m - r;
   int32_t* out = a.kept + ((static_cast<int64_t>(l) * a.src.n_seqs + s) * a.src.n_heads + h) * a.kept_stride;
-  for (int i = tid; i < r; i += T) out[want + i] = n + i;
+  for (int i = c * T + tid; i < r; i += C * T) out[want + i] = n + i;
   if (want == n) {   // none has to go
-    for (int i = tid; i < n; i += T) out[i] = i;
+    for (int i = c * T + tid; i < n; i += C * T) out[i] = i;
     return;
   }
-  if (want <= 0) return;
+  if (want <= 0) return;   // the same in all CTAs of the cluster
   const float* acc = a.acc + l * a.src_layer_rows;
-  const bool fits = n <= max_keys;
+  const int run = (n + C * T - 1) / (C * T) * 32;    // slots of a warp
+  const int c0 = min(c * (T / 32) * run, n), c1 = min(c0 + (T / 32) * run, n);
+  const bool fits = (T / 32) * run <= max_keys;
   auto from_pool = [&](int j) -> uint32_t {
-    const int64_t row = slot_row(a.src, s, h, j);
+    const int row = slot_row(a.src, s, h, j);
     return row < 0 ? 0u : weight_key(acc[row]);
   };
   if (fits) {
 #pragma unroll 4
-    for (int j = tid; j < n; j += T) keys[j] = from_pool(j);
+    for (int j = c0 + tid; j < c1; j += T) keys[j - c0] = from_pool(j);
   }
-  auto key_at = [&](int j) { return fits ? keys[j] : from_pool(j); };
+  auto key_at = [&](int j) { return fits ? keys[j - c0] : from_pool(j); };
   uint32_t bar = 0, mask = 0;
   int rest = want;   // how many of the keys that match bar's known digits are wanted
   for (int shift = 24; shift >= 0; shift -= 8) {
+    int* mine = counts[(shift >> 3) & 1];
     for (int i = tid; i < kSelCopies * 257; i += T) hist[0][i] = 0;
     __syncthreads();   // also: the keys are there
-    for (int j = tid; j < n; j += T) {
+    for (int j = c0 + tid; j < c1; j += T) {
       const uint32_t key = key_at(j);
       if ((key & mask) == bar) atomicAdd(&hist[lane % kSelCopies][(key >> shift) & 255u], 1);
     }
     __syncthreads();
-    // Counts of the bins above: a suffix sum over the 256 bins, in 8 warps.
-    int c = 0, incl = 0;
+    int own = 0;
     if (tid < 256) {
 #pragma unroll
-      for (int k = 0; k < kSelCopies; ++k) c += hist[k][tid];
-      incl = c;
+      for (int k = 0; k < kSelCopies; ++k) own += hist[k][tid];
+      mine[tid] = own;
+    }
+    cluster_sync();
+    // Counts of the bins above: a suffix sum over the 256 bins, in 8 warps.
+    int all = own, incl = 0;
+    if (tid < 256) {
+#pragma unroll
+      for (int k = 1; k < C; ++k) all += ld_cluster(mine + tid, (c + k) % C);
+      incl = all;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int y = __shfl_down_sync(0xffffffffu, incl, off);
@@ -336,10 +362,10 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
     __syncthreads();
     if (tid < 256) {
       for (int w = warp + 1; w < 8; ++w) incl += wsum[0][w];
-      if (incl >= rest && incl - c < rest) {
+      if (incl >= rest && incl - all < rest) {
         s_digit = tid;
-        s_rest = rest - (incl - c);
-        s_whole = s_rest == c;
+        s_rest = rest - (incl - all);
+        s_whole = s_rest == all;
       }
     }
     __syncthreads();
@@ -349,9 +375,9 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
     if (s_whole) break;
   }
   // Keys above the bar are kept, and the first `rest` of its equals (in the
-  // digits looked at).  Each warp owns a run of slots: it counts them, then
-  // writes them behind those of the warps before it.
-  const int run = (n + T - 1) / T * 32, j0 = min(warp * run, n), j1 = min(j0 + run, n);
+  // digits looked at).  Each warp counts them in its run, then writes them
+  // behind those of the warps before it.
+  const int j0 = min(c0 + warp * run, n), j1 = min(j0 + run, n);
   int more = 0, same = 0;
   for (int j = j0 + lane; j < j1; j += 32) {
     const uint32_t key = key_at(j) & mask;
@@ -366,9 +392,22 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
     wsum[1][warp] = same;
   }
   __syncthreads();
-  more = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[0][lane] : 0);
-  same = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[1][lane] : 0);   // equals before this warp
-  int at = more + min(same, rest);
+  const int of = lane < T / 32 ? wsum[0][lane] : 0, os = lane < T / 32 ? wsum[1][lane] : 0;
+  more = __reduce_add_sync(0xffffffffu, lane < warp ? of : 0);
+  same = __reduce_add_sync(0xffffffffu, lane < warp ? os : 0);
+  if constexpr (C > 1) {
+    if (warp == 0) {
+      const int tf = __reduce_add_sync(0xffffffffu, of), ts = __reduce_add_sync(0xffffffffu, os);
+      if (lane == 0) {
+        s_cta[0] = tf;
+        s_cta[1] = ts;
+      }
+    }
+    cluster_sync();
+    more += __reduce_add_sync(0xffffffffu, lane < c ? ld_cluster(&s_cta[0], lane < c ? lane : 0) : 0);
+    same += __reduce_add_sync(0xffffffffu, lane < c ? ld_cluster(&s_cta[1], lane < c ? lane : 0) : 0);
+  }
+  int at = more + min(same, rest);   // `same`: equals before this warp
   for (int j = j0; j < j1; j += 32) {
     const uint32_t key = j + lane < j1 ? key_at(j + lane) & mask : 0u;
     const bool eq = j + lane < j1 && key == bar;
@@ -380,6 +419,7 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
     at += __popc(bt);
     same += __popc(be);
   }
+  if constexpr (C > 1) cluster_sync_all();   // no CTA leaves while another may read its counts
 }
 
 // The kept rows move to the front in slot order: CTA per (layer, head, slice,
@@ -514,17 +554,21 @@ cudaError_t launch_paged_advance(cudaStream_t stream, const PagedView& c, const 
 
 cudaError_t launch_paged_evict(const Launch& L, const EvictArgs& a) {
   const int64_t S = a.src.n_seqs, H = a.src.n_heads, nl = a.n_layers;
-  // Keys in shared memory: all that the tables can hold, up to 48 K.  Few keys
-  // get small CTAs, of which several share an SM.
+  // Few slots: 256 threads a CTA, of which several share an SM.  Many slots
+  // and few (head, sequence, layer): 8 CTAs for each.  Keys in shared memory:
+  // all that the tables can hold, up to 48 K.
   const int64_t cap = static_cast<int64_t>(a.src.max_pages) * a.src.page.d;
-  const int max_keys = static_cast<int>(cap < 49152 ? cap : 49152);
-  const dim3 sel(static_cast<unsigned>(H), static_cast<unsigned>(S), static_cast<unsigned>(nl));
+  const bool wide = cap > 8192 && H * S * nl < L.sm_count;
+  const int64_t own = wide ? (cap + 8191) / 8192 * 1024 : cap;   // slots of a CTA
+  const int max_keys = static_cast<int>(own < 49152 ? own : 49152);
+  const dim3 sel(static_cast<unsigned>(wide ? H * 8 : H), static_cast<unsigned>(S), static_cast<unsigned>(nl));
   // launch_kernel raises a kernel's limit from 48 KB of dynamic shared memory on; the static arrays need room below it.
   size_t smem = static_cast<size_t>(max_keys) * 4;
-  if (smem > 36 * 1024 && smem <= 48 * 1024) smem = 48 * 1024 + 16;
-  cudaError_t e = cap <= 4096
-                      ? launch_kernel(evict_select_kernel<256>, sel, dim3(256), smem, L.stream, a, max_keys)
-                      : launch_kernel(evict_select_kernel<1024>, sel, dim3(1024), smem, L.stream, a, max_keys);
+  if (smem > 32 * 1024 && smem <= 48 * 1024) smem = 48 * 1024 + 16;
+  cudaError_t e =
+      wide          ? launch_kernel(evict_select_kernel<1024, 8>, sel, dim3(1024), smem, L.stream, a, max_keys)
+      : cap <= 4096 ? launch_kernel(evict_select_kernel<256, 1>, sel, dim3(256), smem, L.stream, a, max_keys)
+                    : launch_kernel(evict_select_kernel<1024, 1>, sel, dim3(1024), smem, L.stream, a, max_keys);
   if (e != cudaSuccess) return e;
   // To other pages: whole rows, every block a CTA.  In place: one CTA walks a
   // slice's blocks, so slices (of at least 64 bytes) are cut until there are

@@ -17,12 +17,19 @@ namespace {
 // own tiles of KT keys through its own two cp.async stages (no CTA barrier in
 // the loop; three CTAs an SM are worth more than a third stage), with the page
 // of every row looked up one tile ahead; O is rescaled only when a row's
-// maximum grows by more than 2^8; the four warps' softmax states are joined
-// through shared memory at the end.
+// maximum grows by more than 2^8; the four warps' softmax states, and those of
+// up to 8 CTAs of a sequence (a cluster), are joined through shared memory at
+// the end.
 constexpr int kRowsThreads = 128;
 constexpr int kRowsStages = 2;
 constexpr int kRowsStageBytes = 8192;   // K and V of one warp tile
 constexpr float kRowsSlack = 8.0f;
+
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr, int rank) {   // 8 bytes of the cluster's CTA `rank`
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(map_to_cta(addr, rank)) : "memory");
+  return v;
+}
 
 template <int D, int MT, bool HALF, bool MOD>
 __global__ void __launch_bounds__(kRowsThreads)
@@ -251,10 +258,12 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
   }
   cp_async_wait<0>();
 
-  // Join the four warps (the stages are free once all of them are here).
+  // Join the four warps (the stages are free once all of them are here), then
+  // the CTAs of the cluster, each taking its share of the elements.
   float* sm_m = reinterpret_cast<float*>(smem);          // [4][ROWS]
   float* sm_l = sm_m + 4 * ROWS;                         // [4][ROWS]
-  float* sm_o = sm_l + 4 * ROWS;                         // [4][ROWS][D]
+  float2* sm_ml = reinterpret_cast<float2*>(sm_l + 4 * ROWS);   // [ROWS]: of the CTA
+  float* sm_o = reinterpret_cast<float*>(sm_ml + ROWS);  // [4][ROWS][D], the CTA's own in [0]
   __syncthreads();
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -276,6 +285,20 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
       }
     }
   __syncthreads();
+  auto store = [&](int r, int d, float M, float l, float y0, float y1) {
+    const int t = a.group_div.div(r), h = kh * G + r - t * G;
+    const int64_t tok = q.row0 + t;
+    if (a.parts > 1) {
+      const int64_t pr = (static_cast<int64_t>(sp / a.cluster) * a.ch.n_tokens + tok) * a.n_q_heads + h;
+      if (l != 0.f) *reinterpret_cast<float2*>(a.part_o + pr * D + d) = make_float2(y0, y1);
+      if (d == 0) a.part_ml[pr] = make_float2(M, l);
+    } else {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + tok * a.o_row + h * a.o_head + d) =
+          pack_bf16x2(y0 * inv, y1 * inv);
+      if (d == 0 && a.lse) a.lse[tok * a.n_q_heads + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    }
+  };
   for (int idx = threadIdx.x; idx < rows * (D / 2); idx += kRowsThreads) {
     const int r = idx / (D / 2), d = (idx % (D / 2)) * 2;
     float M = -INFINITY;
@@ -291,19 +314,42 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
       y0 = fmaf(y.x, f, y0);
       y1 = fmaf(y.y, f, y1);
     }
-    const int t = a.group_div.div(r), h = kh * G + r - t * G;
-    const int64_t tok = q.row0 + t;
-    if (a.splits > 1) {
-      const int64_t pr = (static_cast<int64_t>(sp) * a.ch.n_tokens + tok) * a.n_q_heads + h;
-      if (l != 0.f) *reinterpret_cast<float2*>(a.part_o + pr * D + d) = make_float2(y0, y1);
-      if (d == 0) a.part_ml[pr] = make_float2(M, l);
+    if (a.cluster == 1) {
+      store(r, d, M, l, y0, y1);
     } else {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + tok * a.o_row + h * a.o_head + d) =
-          pack_bf16x2(y0 * inv, y1 * inv);
-      if (d == 0 && a.lse) a.lse[tok * a.n_q_heads + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+      *reinterpret_cast<float2*>(sm_o + r * D + d) = make_float2(y0, y1);   // only this thread reads [.][r][d]
+      if (d == 0) sm_ml[r] = make_float2(M, l);
     }
   }
+  if (a.cluster == 1) return;
+  cluster_sync_all();
+  const int rank = sp % a.cluster;
+  for (int idx = rank * kRowsThreads + threadIdx.x; idx < rows * (D / 2); idx += a.cluster * kRowsThreads) {
+    const int r = idx / (D / 2), d = (idx % (D / 2)) * 2;
+    const uint32_t ml_at = smem_addr(sm_ml + r), y_at = smem_addr(sm_o + r * D + d);
+    float2 ml[8], y[8];
+    float M = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      ml[c] = make_float2(-INFINITY, 0.f);
+      if (c < a.cluster) {
+        ml[c] = ld_cluster2(ml_at, c);
+        y[c] = ld_cluster2(y_at, c);
+        M = fmaxf(M, ml[c].x);
+      }
+    }
+    float l = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (ml[c].y == 0.f) continue;
+      const float f = ex2_approx(ml[c].x - M);
+      l = fmaf(ml[c].y, f, l);
+      y0 = fmaf(y[c].x, f, y0);
+      y1 = fmaf(y[c].y, f, y1);
+    }
+    store(r, d, M, l, y0, y1);
+  }
+  cluster_sync_all();   // no CTA leaves while another may read its results
 }
 
 // ------------------------------------------------------------------- fp32 --
@@ -434,7 +480,7 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
     if (r >= rows) continue;
     const int t = a.group_div.div(r), h = kh * G + r - t * G;
     const int64_t tok = q.row0 + t;
-    if (a.splits > 1) {
+    if (a.parts > 1) {
       const int64_t pr = (static_cast<int64_t>(sp) * a.ch.n_tokens + tok) * a.n_q_heads + h;
 #pragma unroll
       for (int e = 0; e < V; ++e) a.part_o[pr * D + lane * V + e] = acc[j][e];
@@ -486,7 +532,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine_kernel(con
 #pragma unroll
     for (int i = 0; i < kMaxSplits / 32; ++i) {
       const int sp = i * 32 + lane;
-      ml[i] = sp < a.splits ? a.part_ml[sp * rows + row] : make_float2(-INFINITY, 0.f);
+      ml[i] = sp < a.parts ? a.part_ml[sp * rows + row] : make_float2(-INFINITY, 0.f);
       M = fmaxf(M, ml[i].x);
     }
 #pragma unroll
@@ -501,13 +547,13 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine_kernel(con
     for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
 #pragma unroll
     for (int i = 0; i < kMaxSplits / 32; ++i)
-      for (int j0 = w; j0 < 32 && i * 32 + j0 < a.splits; j0 += W * kCombineDeep) {
+      for (int j0 = w; j0 < 32 && i * 32 + j0 < a.parts; j0 += W * kCombineDeep) {
         float x[kCombineDeep][V], ws[kCombineDeep];
 #pragma unroll
         for (int k = 0; k < kCombineDeep; ++k) {
           const int j = j0 + k * W, sp = i * 32 + j;
           ws[k] = __shfl_sync(0xffffffffu, wt[i], j & 31);
-          if (j >= 32 || sp >= a.splits) ws[k] = 0.f;
+          if (j >= 32 || sp >= a.parts) ws[k] = 0.f;
           const float* src = a.part_o + (sp * rows + row) * D + lane * V;
 #pragma unroll
           for (int e = 0; e < V; ++e) x[k][e] = ws[k] == 0.f ? 0.f : src[e];   // an empty part wrote no output
@@ -852,10 +898,11 @@ template <int D, int MT, bool HALF, bool MOD>
 cudaError_t launch_rows(const Launch& L, const PagedAttnArgs& a) {
   constexpr size_t ring = 4 * kRowsStages * kRowsStageBytes;
   constexpr size_t rows = HALF ? 8 : 16 * MT;
-  constexpr size_t join = (2 * 4 * rows + 4 * rows * D) * sizeof(float);
+  constexpr size_t join = (10 * rows + 4 * rows * D) * sizeof(float);
   constexpr size_t smem = ring > join ? ring : join;
   const dim3 grid(a.splits, a.c.n_heads, a.c.n_seqs);
-  return launch_kernel(paged_attn_rows_kernel<D, MT, HALF, MOD>, grid, dim3(kRowsThreads), smem, L.stream, a);
+  return launch_clusters(paged_attn_rows_kernel<D, MT, HALF, MOD>, grid, dim3(kRowsThreads), smem, L.stream, a.cluster,
+                         a);
 }
 template <int D, bool MOD>
 cudaError_t launch_rows_d(const Launch& L, const PagedAttnArgs& a) {
@@ -870,7 +917,7 @@ template <int D, bool BF16>
 cudaError_t launch_combine(const Launch& L, const PagedAttnArgs& a) {
   const int64_t rows = static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
   const dim3 block(kCombineThreads);
-  if (rows <= 8 * L.sm_count && a.splits >= 16)
+  if (rows <= 8 * L.sm_count && a.parts >= 16)
     return launch_kernel(paged_attn_combine_kernel<D, BF16, 8>, dim3(static_cast<unsigned>(rows)), block, 0, L.stream, a);
   return launch_kernel(paged_attn_combine_kernel<D, BF16, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), block, 0,
                        L.stream, a);

@@ -498,7 +498,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
           if (!mine) continue;
-          if (a.splits > 1) {
+          if (a.parts > 1) {
             float* dst = a.part_o + pr * D + c * 32;
             if (!empty)
 #pragma unroll
@@ -514,7 +514,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           }
         }
         if (mine) {
-          if (a.splits > 1) a.part_ml[pr] = make_float2(m_used, l_run);
+          if (a.parts > 1) a.part_ml[pr] = make_float2(m_used, l_run);
           else if (a.lse) a.lse[tok * a.n_q_heads + h] = empty ? -INFINITY : (m_used + log2f(l_run)) * kLn2;
         }
       }

@@ -53,6 +53,31 @@ cudaError_t launch_kernel(void (*k)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
 }
 
+// The same in clusters of `cluster` CTAs along x.
+template <class... KArgs, class... Args>
+cudaError_t launch_clusters(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
+                            Args&&... args) {
+  if (cluster == 1) return launch_kernel(k, grid, block, smem, stream, std::forward<Args>(args)...);
+  if (smem > 48 * 1024) {
+    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(k), smem)) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
+}
+
 // ------------------------------------------------------------- tracing --
 // Every kernel launch goes through traced(): it counts the launches and,
 // while tracing is enabled for the calling thread (vx_trace_enable), brackets

@@ -145,9 +145,11 @@ struct PagedAttnArgs {
   int64_t score_stride;    // of list positions, a multiple of 4
   float* part_w;           // [w_segs][n_seqs][n_heads][part_stride] (w_segs > 1)
   int64_t part_stride;     // slots
-  int splits;              // parts of every sequence's key range
-  float* part_o;           // [splits][n_tokens][n_q_heads][head_dim] (splits > 1)
-  float2* part_ml;         // [splits][n_tokens][n_q_heads]: running max (log2) and sum
+  int splits;              // CTAs that every sequence's key range is cut into
+  int cluster;             // of them join their results in shared memory (rows kernel)
+  int parts;               // splits / cluster: results left to the combining kernel
+  float* part_o;           // [parts][n_tokens][n_q_heads][head_dim] (parts > 1)
+  float2* part_ml;         // [parts][n_tokens][n_q_heads]: running max (log2) and sum
   DevStatus* status;
   uint64_t limit_ns;
 };
@@ -155,7 +157,8 @@ struct PagedAttnArgs {
 // Which kernel runs and into how many parts the keys are split.
 struct PagedAttnPlan {
   int kernel;    // 0: warp-level rows kernel, 1: tcgen05 kernel, 2: fp32 kernel
-  int splits;
+  int splits;    // CTAs that every sequence's key range is cut into
+  int cluster;   // of them that join their results themselves (1, 2, 4 or 8)
   int w_segs;    // segments of the rows in the sum of the weights (track)
   bool keep_scores;   // the rows kernel leaves its scores for the sum of the weights (track)
 };

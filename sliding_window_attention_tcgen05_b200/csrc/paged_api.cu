@@ -24,8 +24,9 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
   int64_t want, min_keys, ctas;
   if (!bf16) {
     p.kernel = 2;
-    ctas = lanes * ((rows + 15) / 16);
-    want = 4 * kPlanSms;
+    const int block = f32_block_rows(rows);
+    ctas = lanes * ((rows + block - 1) / block);
+    want = block == 64 ? 2 * kPlanSms : 6 * kPlanSms;
     min_keys = 128;
   } else if (rows <= 32) {
     // A row block of the tcgen05 kernel would be at least three quarters padding.

@@ -138,4 +138,7 @@ cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, b
 
 constexpr int kMaxSplits = 64;
 
+// Rows of a block of the fp32 kernel, for sequences of up to `rows` rows.
+inline int f32_block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
 }  // namespace vx

@@ -353,145 +353,197 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
 }
 
 // ------------------------------------------------------------------- fp32 --
-// paged_attn_f32_kernel: CTA per (16-row block x key range, K/V head,
-// sequence), four warps of four rows each; 32-key tiles of K (padded rows) and
-// V in shared memory, scores with one key per lane, P V with D / 32 dims per
-// lane.  CUDA cores throughout: tensor-core tf32 would keep 10 mantissa bits.
-constexpr int kF32Rows = 16;
-constexpr int kF32Keys = 32;
+// paged_attn_f32_kernel: CTA per (block of 16 * RM rows x key range, K/V head,
+// sequence), CUDA cores throughout (tensor-core tf32 would keep 10 mantissa
+// bits).  256 threads as 16 x 16: a thread computes RM rows x 4 keys of a
+// 64-key tile's scores and RM rows x D / 16 dims of the output, so that shared
+// memory is read once for 8 (RM 4) or 4 multiply-adds; the V tile travels
+// while the scores are computed and the next K tile while P V is.  RM follows
+// the number of rows; at RM 1 the shared-memory reads bound it.
+constexpr int kF32Threads = 256;
+constexpr int kF32Keys = 64;
 
-template <int D>
-__global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
+template <int D, int RM>
+struct F32Cfg {
+  static constexpr int kRows = 16 * RM;
+  static constexpr int kPitch = D + 4;          // of Q and K rows: neighbouring rows 16 bytes apart modulo the banks
+  static constexpr int kPPitch = kF32Keys + 4;
+  static constexpr size_t kSmem =
+      (static_cast<size_t>(kRows + kF32Keys) * kPitch + kF32Keys * D + kRows * kPPitch) * 4 + 2 * kF32Keys * 4;
+};
+
+// Pool rows of the tile at list position xt (thread = key), -1 where there is none.
+__device__ __forceinline__ int f32_row(const PagedAttnArgs& a, const KeyList& kl, int s, int kh, int x, int x1) {
+  if (x >= x1) return -1;
+  const int r = slot_row(a.c, s, kh, key_slot(kl, x));
+  if (r < 0) report_bad_cache(a.status, s);
+  return r;
+}
+// A tile's rows (PITCH floats apart in shared memory) by cp.async; the caller commits.
+template <int D, int PITCH>
+__device__ __forceinline__ void f32_tile(uint32_t dst, const float* pool, const int* rows) {
+  for (int i = threadIdx.x; i < kF32Keys * (D / 4); i += kF32Threads) {
+    const int r = i / (D / 4), c = i % (D / 4), gr = rows[r];
+    cp_async16(dst + (r * PITCH + c * 4) * 4, pool + static_cast<int64_t>(max(gr, 0)) * D + c * 4, gr >= 0);
+  }
+}
+
+template <int D, int RM>
+__global__ void __launch_bounds__(kF32Threads) paged_attn_f32_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
   pdl_wait();
   pdl_trigger();
-  constexpr int KP = D + 4;        // padded K row: 16-byte reads of 32 rows hit all banks evenly
-  constexpr int V = D / 32;
-  __shared__ __align__(16) float sq[kF32Rows][D];
-  __shared__ __align__(16) float sk[kF32Keys][KP];
-  __shared__ __align__(16) float sv[kF32Keys][D];
-  __shared__ __align__(16) float spr[kF32Rows][kF32Keys];
+  using Cfg = F32Cfg<D, RM>;
+  constexpr int R = Cfg::kRows, KP = Cfg::kPitch, PP = Cfg::kPPitch, DV = D / 64;
+  extern __shared__ __align__(16) float fsm[];
+  float* sq = fsm;                       // [R][KP]
+  float* sk = sq + R * KP;               // [64][KP]
+  float* sv = sk + kF32Keys * KP;        // [64][D]
+  float* spr = sv + kF32Keys * D;        // [R][PP]
+  int* s_row = reinterpret_cast<int*>(spr + R * PP);   // [2][64]
   const int rb = blockIdx.x % blocks, sp = blockIdx.x / blocks, kh = blockIdx.y, s = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const SeqSpan q = seq_span(a.c, a.ch, s);
-  const int G = a.group, rows = q.n * G, r0 = rb * kF32Rows;
+  const int G = a.group, rows = q.n * G, r0 = rb * R;
   if (r0 >= rows) return;
-  if (q.over && threadIdx.x == 0) report_bad_cache(a.status, s);
-  const int rn = min(kF32Rows, rows - r0);
+  if (q.over && tid == 0) report_bad_cache(a.status, s);
+  const int rn = min(R, rows - r0);
   const int tf = a.group_div.div(r0), tl = a.group_div.div(r0 + rn - 1);
   const KeyList kl = key_list(q.old + tf, q.old + tl, a.window, a.prefix ? a.prefix[s] : 0, q.kv);
   const int step = ((kl.total + a.splits - 1) / a.splits + kF32Keys - 1) / kF32Keys * kF32Keys;
   const int x0 = min(sp * step, kl.total), x1 = min(x0 + step, kl.total);
+  const int tiles = (x1 - x0 + kF32Keys - 1) / kF32Keys;
   const float* kp = static_cast<const float*>(a.k);
   const float* vp = static_cast<const float*>(a.v);
-  for (int i = threadIdx.x; i < kF32Rows * (D / 4); i += 128) {
+  if (tid < kF32Keys) s_row[tid] = f32_row(a, kl, s, kh, x0 + tid, x1);
+  for (int i = tid; i < R * (D / 4); i += kF32Threads) {
     const int r = i / (D / 4), c = i % (D / 4);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rn) {
-      const int t = a.group_div.div(r0 + r), h = kh * G + r0 + r - t * G;
-      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head +
-                                           c * 4);
-    }
-    *reinterpret_cast<float4*>(&sq[r][c * 4]) = x;
+    const bool ok = r < rn;
+    const int t = a.group_div.div(r0 + (ok ? r : 0)), h = kh * G + r0 + (ok ? r : 0) - t * G;
+    cp_async16(smem_addr(sq + r * KP + c * 4),
+               static_cast<const float*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head + c * 4, ok);
   }
+  __syncthreads();
+  if (tiles > 0) f32_tile<D, KP>(smem_addr(sk), kp, s_row);
+  cp_async_commit();
   const ScoreMod sm = score_mod(a);
-  int qi[4];
-  float slope2[4], m[4], l[4], acc[4][V];
+  int qi[RM];
+  float slope2[RM], m[RM], l[RM], o[RM][4 * DV];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = min(r0 + warp * 4 + j, rows - 1);
+  for (int i = 0; i < RM; ++i) {
+    const int r = min(r0 + ty * RM + i, rows - 1);
     const int t = a.group_div.div(r);
-    qi[j] = q.old + t;
-    slope2[j] = a.slopes ? a.slopes[kh * G + r - t * G] * kLog2e : 0.f;
-    m[j] = -INFINITY;
-    l[j] = 0.f;
+    qi[i] = q.old + t;
+    slope2[i] = a.slopes ? a.slopes[kh * G + r - t * G] * kLog2e : 0.f;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[j][e] = 0.f;
+    for (int e = 0; e < 4 * DV; ++e) o[i][e] = 0.f;
   }
-  for (int xt = x0; xt < x1; xt += kF32Keys) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kF32Keys * (D / 4); i += 128) {
-      const int r = i / (D / 4), c = i % (D / 4);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (xt + r < x1) {
-        const int gr = slot_row(a.c, s, kh, key_slot(kl, xt + r));
-        if (gr >= 0) {
-          x = *reinterpret_cast<const float4*>(kp + static_cast<int64_t>(gr) * D + c * 4);
-          y = *reinterpret_cast<const float4*>(vp + static_cast<int64_t>(gr) * D + c * 4);
-        } else {
-          report_bad_cache(a.status, s);
-        }
-      }
-      *reinterpret_cast<float4*>(&sk[r][c * 4]) = x;
-      *reinterpret_cast<float4*>(&sv[r][c * 4]) = y;
-    }
-    __syncthreads();
-    float dot[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int c = 0; c < D / 4; ++c) {
-      const float4 kk = *reinterpret_cast<const float4*>(&sk[lane][c * 4]);
+  for (int u = 0; u < tiles; ++u) {
+    const int xt = x0 + u * kF32Keys;
+    int* row = s_row + (u & 1) * kF32Keys;
+    cp_async_wait<0>();
+    __syncthreads();                     // K (and Q) of this tile have landed, V's buffer is free
+    f32_tile<D, D>(smem_addr(sv), vp, row);
+    cp_async_commit();
+    if (tid < kF32Keys && u + 1 < tiles) s_row[((u + 1) & 1) * kF32Keys + tid] = f32_row(a, kl, s, kh, xt + kF32Keys + tid, x1);
+    float sc[RM][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 qq = *reinterpret_cast<const float4*>(&sq[warp * 4 + j][c * 4]);
-        dot[j] = fmaf(qq.x, kk.x, dot[j]);
-        dot[j] = fmaf(qq.y, kk.y, dot[j]);
-        dot[j] = fmaf(qq.z, kk.z, dot[j]);
-        dot[j] = fmaf(qq.w, kk.w, dot[j]);
-      }
-    }
-    const int x = xt + lane, js = key_slot(kl, x);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool seen = x < x1 && (js < kl.pre || (js <= qi[j] && js > qi[j] - a.window));
-      const float v = seen ? score2(sm, dot[j], slope2[j], qi[j] - js) : -INFINITY;
-      float cmax = v;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, off));
-      const float m_new = fmaxf(m[j], cmax);
-      const float mu = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = exp2f(m[j] - mu);
-      const float p = exp2f(v - mu);
-      float ps = p;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
-      m[j] = m_new;
-      l[j] = l[j] * alpha + ps;
-      spr[warp * 4 + j][lane] = p;
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[j][e] *= alpha;
-    }
-    __syncwarp();
+    for (int i = 0; i < RM; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll 4
-    for (int kk = 0; kk < kF32Keys; ++kk) {
-      float vv[V];
+    for (int d = 0; d < D; d += 4) {
+      float4 kk[4], qq[RM];
 #pragma unroll
-      for (int e = 0; e < V; ++e) vv[e] = sv[kk][lane * V + e];
+      for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * KP + d);
+#pragma unroll
+      for (int i = 0; i < RM; ++i) qq[i] = *reinterpret_cast<const float4*>(sq + (ty * RM + i) * KP + d);
+#pragma unroll
+      for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sc[i][j] = fmaf(qq[i].x, kk[j].x, sc[i][j]);
+          sc[i][j] = fmaf(qq[i].y, kk[j].y, sc[i][j]);
+          sc[i][j] = fmaf(qq[i].z, kk[j].z, sc[i][j]);
+          sc[i][j] = fmaf(qq[i].w, kk[j].w, sc[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      float cmax = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = spr[warp * 4 + j][kk];
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[j][e] = fmaf(p, vv[e], acc[j][e]);
+        const int x = xt + tx + 16 * j, js = key_slot(kl, x);
+        const bool seen = x < x1 && (js < kl.pre || (js <= qi[i] && js > qi[i] - a.window));
+        sc[i][j] = seen ? score2(sm, sc[i][j], slope2[i], qi[i] - js) : -INFINITY;
+        cmax = fmaxf(cmax, sc[i][j]);
       }
-    }
-    __syncwarp();
-  }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = r0 + warp * 4 + j;
+      for (int off = 8; off > 0; off >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, off));
+      const float m_new = fmaxf(m[i], cmax);
+      const float mu = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m[i] - mu);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(sc[i][j] - mu);
+        spr[(ty * RM + i) * PP + tx + 16 * j] = p;
+        sum += p;
+      }
+      m[i] = m_new;
+      l[i] = l[i] * alpha + sum;         // of this thread's keys
+#pragma unroll
+      for (int e = 0; e < 4 * DV; ++e) o[i][e] *= alpha;
+    }
+    cp_async_wait<0>();
+    __syncthreads();                     // V has landed, P is written, K's buffer is free
+    if (u + 1 < tiles) f32_tile<D, KP>(smem_addr(sk), kp, s_row + ((u + 1) & 1) * kF32Keys);
+    cp_async_commit();
+#pragma unroll 2
+    for (int key = 0; key < kF32Keys; key += 4) {
+      float4 p[RM];
+#pragma unroll
+      for (int i = 0; i < RM; ++i) p[i] = *reinterpret_cast<const float4*>(spr + (ty * RM + i) * PP + key);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int e = 0; e < DV; ++e) {
+          const float4 v = *reinterpret_cast<const float4*>(sv + (key + kk) * D + tx * 4 + 64 * e);
+#pragma unroll
+          for (int i = 0; i < RM; ++i) {
+            const float pk = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+            o[i][4 * e] = fmaf(pk, v.x, o[i][4 * e]);
+            o[i][4 * e + 1] = fmaf(pk, v.y, o[i][4 * e + 1]);
+            o[i][4 * e + 2] = fmaf(pk, v.z, o[i][4 * e + 2]);
+            o[i][4 * e + 3] = fmaf(pk, v.w, o[i][4 * e + 3]);
+          }
+        }
+    }
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const int r = r0 + ty * RM + i;
+    float sum = l[i];
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if (r >= rows) continue;
     const int t = a.group_div.div(r), h = kh * G + r - t * G;
     const int64_t tok = q.row0 + t;
+    float inv = 1.f;
+    float* dst;
     if (a.parts > 1) {
       const int64_t pr = (static_cast<int64_t>(sp) * a.ch.n_tokens + tok) * a.n_q_heads + h;
-#pragma unroll
-      for (int e = 0; e < V; ++e) a.part_o[pr * D + lane * V + e] = acc[j][e];
-      if (lane == 0) a.part_ml[pr] = make_float2(m[j], l[j]);
+      dst = a.part_o + pr * D;
+      if (tx == 0) a.part_ml[pr] = make_float2(m[i], sum);
     } else {
-      const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
-      float* dst = static_cast<float*>(a.o) + tok * a.o_row + h * a.o_head;
-#pragma unroll
-      for (int e = 0; e < V; ++e) dst[lane * V + e] = acc[j][e] * inv;
-      if (lane == 0 && a.lse) a.lse[tok * a.n_q_heads + h] = l[j] == 0.f ? -INFINITY : (m[j] + log2f(l[j])) * kLn2;
+      inv = sum == 0.f ? 0.f : 1.f / sum;
+      dst = static_cast<float*>(a.o) + tok * a.o_row + h * a.o_head;
+      if (tx == 0 && a.lse) a.lse[tok * a.n_q_heads + h] = sum == 0.f ? -INFINITY : (m[i] + log2f(sum)) * kLn2;
     }
+#pragma unroll
+    for (int e = 0; e < DV; ++e)
+      *reinterpret_cast<float4*>(dst + tx * 4 + 64 * e) =
+          make_float4(o[i][4 * e] * inv, o[i][4 * e + 1] * inv, o[i][4 * e + 2] * inv, o[i][4 * e + 3] * inv);
   }
 }
 
@@ -819,20 +871,25 @@ __global__ void __launch_bounds__(128) paged_attn_weights_sum_kernel(const __gri
   add_weight(a, slot_row(a.c, s, kh, j), x);
 }
 
-// fp32: CTA per 32 slots (and segment of their rows); a lane owns a slot, each warp every fourth row.
-constexpr int kWKeysF32 = 32;
+// fp32: CTA per 64 slots (and segment of their rows), 256 threads as 16 x 16,
+// four rows x four slots each, the rows past in double-buffered blocks of 64.
+constexpr int kWKeysF32 = kF32Keys;
 
 template <int D>
-__global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __grid_constant__ PagedAttnArgs a) {
+__global__ void __launch_bounds__(kF32Threads) paged_attn_weights_f32_kernel(const __grid_constant__ PagedAttnArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int KP = D + 4;
-  __shared__ __align__(16) float sk[32][KP];
-  __shared__ __align__(16) float sq[4][D];
-  __shared__ float part[4][32];
+  extern __shared__ __align__(16) float fsm[];
+  float* sk = fsm;                                        // [64][KP]
+  float* sq = sk + kWKeysF32 * KP;                        // [2][64][KP]
+  float* part = sq;                                       // [16][64], after the last block
+  float* s_lse = sq + 2 * kWRows * KP;                    // [2][64]
+  float* s_sl = s_lse + 2 * kWRows;                       // [2][64]
+  int* s_i = reinterpret_cast<int*>(s_sl + 2 * kWRows);   // [2][64]
   const int kh = blockIdx.y, s = blockIdx.z;
   const int seg = blockIdx.x % a.w_segs, tile0 = blockIdx.x / a.w_segs, tiles = gridDim.x / a.w_segs;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const SeqSpan q = seq_span(a.c, a.ch, s);
   if (q.n <= 0) return;
   const int G = a.group;
@@ -842,55 +899,94 @@ __global__ void __launch_bounds__(128) paged_attn_weights_f32_kernel(const __gri
     const int j0 = tile * kWKeysF32, j1 = min(j0 + kWKeysF32, q.kv);
     const bool cut = a.w_segs > 1 && j1 <= a.part_stride;
     if (!cut && seg > 0) continue;
-    __syncthreads();
-    for (int i = tid; i < 32 * (D / 4); i += 128) {
-      const int r = i / (D / 4), c = i % (D / 4);
-      const int gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
-      *reinterpret_cast<float4*>(&sk[r][c * 4]) =
-          gr >= 0 ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + static_cast<int64_t>(gr) * D + c * 4)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    __syncthreads();
-    const int j = j0 + lane;
+    // Tokens that see some slot of the tile.
     int t0 = max(0, j0 - q.old), t1 = min(q.n, j1 - 1 - q.old + min(a.window, kNoWindow - 1 - j1));
     if (j0 < pre) { t0 = 0; t1 = q.n; }
     int ra = t0 * G, rz = max(t1 * G, ra);
     if (cut) {
-      const int64_t all = rz - ra;
-      rz = ra + static_cast<int>(all * (seg + 1) / a.w_segs);
-      ra += static_cast<int>(all * seg / a.w_segs);
+      const int64_t all = (rz - ra + kWRows - 1) / kWRows;
+      const int b0 = static_cast<int>(all * seg / a.w_segs), b1 = static_cast<int>(all * (seg + 1) / a.w_segs);
+      rz = min(rz, ra + b1 * kWRows);
+      ra += b0 * kWRows;
     }
-    float sum = 0.f;
-    for (int r = ra + warp; r < rz; r += 4) {
-      const int t = a.group_div.div(r), h = kh * G + r - t * G;
-      const float* src = static_cast<const float*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head;
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) sq[warp][e * 32 + lane] = src[e * 32 + lane];
-      __syncwarp();
-      float dot = 0.f;
-#pragma unroll 8
-      for (int c = 0; c < D / 4; ++c) {
-        const float4 kk = *reinterpret_cast<const float4*>(&sk[lane][c * 4]);
-        const float4 qq = *reinterpret_cast<const float4*>(&sq[warp][c * 4]);
-        dot = fmaf(qq.x, kk.x, dot);
-        dot = fmaf(qq.y, kk.y, dot);
-        dot = fmaf(qq.z, kk.z, dot);
-        dot = fmaf(qq.w, kk.w, dot);
+    const int blocks = (rz - ra + kWRows - 1) / kWRows;
+    auto stage_q = [&](int blk, int buf) {
+      const int rbase = ra + blk * kWRows;
+      for (int i = tid; i < kWRows * (D / 4); i += kF32Threads) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        const bool ok = rbase + r < rz;
+        const int t = a.group_div.div(ok ? rbase + r : 0), h = kh * G + (ok ? rbase + r : 0) - t * G;
+        cp_async16(smem_addr(sq + (buf * kWRows + r) * KP + c * 4),
+                   static_cast<const float*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head + c * 4, ok);
       }
-      const int i = q.old + t;
-      const float z = a.lse[static_cast<int64_t>(q.row0 + t) * a.n_q_heads + h];
-      const bool seen = z != -INFINITY && (j < pre || (j <= i && j > i - a.window));
-      const float v = score2(sm, dot, a.slopes ? a.slopes[h] * kLog2e : 0.f, i - j);
-      sum += seen ? exp2f(v - z * kLog2e) : 0.f;
+      if (tid < kWRows) {
+        const bool ok = rbase + tid < rz;
+        const int t = a.group_div.div(ok ? rbase + tid : 0), h = kh * G + (ok ? rbase + tid : 0) - t * G;
+        const float z = ok ? a.lse[static_cast<int64_t>(q.row0 + t) * a.n_q_heads + h] : -INFINITY;
+        s_lse[buf * kWRows + tid] = z == -INFINITY ? INFINITY : z * kLog2e;   // weight 0 without a sum
+        s_i[buf * kWRows + tid] = q.old + t;
+        s_sl[buf * kWRows + tid] = a.slopes ? a.slopes[h] * kLog2e : 0.f;
+      }
+      cp_async_commit();
+    };
+    if (blocks > 0) {
+      for (int i = tid; i < kWKeysF32 * (D / 4); i += kF32Threads) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        const int gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
+        cp_async16(smem_addr(sk + r * KP + c * 4),
+                   static_cast<const float*>(a.k) + static_cast<int64_t>(max(gr, 0)) * D + c * 4, gr >= 0);
+      }
+      stage_q(0, 0);
     }
-    part[warp][lane] = sum;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int blk = 0; blk < blocks; ++blk) {
+      const int buf = blk & 1;
+      cp_async_wait<0>();
+      __syncthreads();
+      if (blk + 1 < blocks) stage_q(blk + 1, buf ^ 1);
+      float sc[4][4] = {};
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 kk[4], qq[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * KP + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qq[i] = *reinterpret_cast<const float4*>(sq + (buf * kWRows + ty * 4 + i) * KP + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sc[i][j] = fmaf(qq[i].x, kk[j].x, sc[i][j]);
+            sc[i][j] = fmaf(qq[i].y, kk[j].y, sc[i][j]);
+            sc[i][j] = fmaf(qq[i].z, kk[j].z, sc[i][j]);
+            sc[i][j] = fmaf(qq[i].w, kk[j].w, sc[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = buf * kWRows + ty * 4 + i, pos = s_i[col];
+        const float z = s_lse[col], sl = s_sl[col];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int slot = j0 + tx + 16 * j;
+          const bool seen = slot < pre || (slot <= pos && slot > pos - a.window);
+          sum[j] += seen ? exp2f(score2(sm, sc[i][j], sl, pos - slot) - z) : 0.f;
+        }
+      }
+    }
+    cp_async_wait<0>();
+    __syncthreads();                     // the blocks' buffer becomes the sums'
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[ty * kWKeysF32 + tx + 16 * j] = sum[j];
     __syncthreads();
-    if (warp == 0 && j < j1) {
-      const float x = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
-      if (cut) weight_part(a, seg, s, kh)[j] = x;
-      else add_weight(a, slot_row(a.c, s, kh, j), x);
+    if (tid < kWKeysF32 && j0 + tid < j1) {
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x += part[k * kWKeysF32 + tid];
+      if (cut) weight_part(a, seg, s, kh)[j0 + tid] = x;
+      else add_weight(a, slot_row(a.c, s, kh, j0 + tid), x);
     }
+    __syncthreads();
   }
 }
 
@@ -910,6 +1006,19 @@ cudaError_t launch_rows_d(const Launch& L, const PagedAttnArgs& a) {
   return rows <= 8    ? launch_rows<D, 1, true, MOD>(L, a)
          : rows <= 16 ? launch_rows<D, 1, false, MOD>(L, a)
                       : launch_rows<D, 2, false, MOD>(L, a);
+}
+
+template <int D, int RM>
+cudaError_t launch_f32(const Launch& L, const PagedAttnArgs& a) {
+  constexpr int R = F32Cfg<D, RM>::kRows;
+  const int blocks = static_cast<int>((static_cast<int64_t>(a.ch.max_q) * a.group + R - 1) / R);
+  const dim3 grid(static_cast<unsigned>(blocks) * a.splits, a.c.n_heads, a.c.n_seqs);
+  return launch_kernel(paged_attn_f32_kernel<D, RM>, grid, dim3(kF32Threads), F32Cfg<D, RM>::kSmem, L.stream, a, blocks);
+}
+template <int D>
+cudaError_t launch_weights_f32(const Launch& L, const PagedAttnArgs& a, const dim3& grid) {
+  constexpr size_t smem = (static_cast<size_t>(kWKeysF32 + 2 * kWRows) * (D + 4) + 3 * 2 * kWRows) * 4;
+  return launch_kernel(paged_attn_weights_f32_kernel<D>, grid, dim3(kF32Threads), smem, L.stream, a);
 }
 
 // Few rows get eight warps each, so that their parts are read by several SMs' worth of loads at once.
@@ -938,10 +1047,10 @@ cudaError_t launch_paged_attn_rows(const Launch& L, const PagedAttnArgs& a) {
 }
 
 cudaError_t launch_paged_attn_f32(const Launch& L, const PagedAttnArgs& a) {
-  const int blocks = static_cast<int>((static_cast<int64_t>(a.ch.max_q) * a.group + kF32Rows - 1) / kF32Rows);
-  const dim3 grid(static_cast<unsigned>(blocks) * a.splits, a.c.n_heads, a.c.n_seqs);
-  return a.head_dim == 128 ? launch_kernel(paged_attn_f32_kernel<128>, grid, dim3(128), 0, L.stream, a, blocks)
-                           : launch_kernel(paged_attn_f32_kernel<64>, grid, dim3(128), 0, L.stream, a, blocks);
+  const int rows = f32_block_rows(static_cast<int64_t>(a.ch.max_q) * a.group);
+  if (a.head_dim == 128)
+    return rows == 16 ? launch_f32<128, 1>(L, a) : rows == 32 ? launch_f32<128, 2>(L, a) : launch_f32<128, 4>(L, a);
+  return rows == 16 ? launch_f32<64, 1>(L, a) : rows == 32 ? launch_f32<64, 2>(L, a) : launch_f32<64, 4>(L, a);
 }
 
 cudaError_t launch_paged_attn_combine(const Launch& L, const PagedAttnArgs& a, bool bf16) {
@@ -960,8 +1069,7 @@ cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, b
   const dim3 grid(static_cast<unsigned>((max_kv + keys - 1) / keys * a.w_segs), a.c.n_heads, a.c.n_seqs);
   cudaError_t e;
   if (!bf16)
-    e = a.head_dim == 128 ? launch_kernel(paged_attn_weights_f32_kernel<128>, grid, dim3(128), 0, L.stream, a)
-                          : launch_kernel(paged_attn_weights_f32_kernel<64>, grid, dim3(128), 0, L.stream, a);
+    e = a.head_dim == 128 ? launch_weights_f32<128>(L, a, grid) : launch_weights_f32<64>(L, a, grid);
   else if (a.head_dim == 128)
     e = mod ? launch_weights<128, true>(L, a, grid) : launch_weights<128, false>(L, a, grid);
   else

@@ -44,13 +44,18 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
   const int64_t most = max_kv / min_keys;
   if (sp > most) sp = most;
   if (sp > kMaxSplits) sp = kMaxSplits;
-  // Where all of the rows kernel's CTAs run at once (three an SM), clusters of up to 8 join their results themselves,
-  // which saves the combining launch; with more CTAs than that a cluster holds its places on the SMs until its slowest
-  // CTA is done (64 sequences of up to 4096 tokens, 8 K/V heads: 96 us in clusters of 4, 92 us without).
+  // Where the rows kernel's CTAs can all run at once (three an SM) with few enough keys each, clusters of up to 8 join
+  // their results themselves, which saves the combining launch; with more CTAs than that a cluster holds its places on
+  // the SMs until its slowest CTA is done (64 sequences of up to 4096 tokens, 8 K/V heads: 96 us in clusters of 4, 92 us
+  // without).
   p.cluster = 1;
-  if (p.kernel == 0 && sp > 1 && ctas * sp <= 3 * kPlanSms) {
-    p.cluster = sp >= 8 ? 8 : sp > 3 ? 4 : 2;
-    sp = sp / p.cluster * p.cluster;
+  if (p.kernel == 0) {
+    int c = 8;
+    while (c > 1 && (ctas * c > 3 * kPlanSms || max_kv < c * 64)) c /= 2;
+    if (max_kv <= c * 512 || sp <= c) {
+      p.cluster = c;
+      sp = c;
+    }
   }
   p.splits = static_cast<int>(sp < 1 ? 1 : sp);
   // Sum of the weights: segments until there are a few CTAs for each place on the SMs (8 of 128 threads each), none

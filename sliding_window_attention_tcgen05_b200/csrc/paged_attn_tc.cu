@@ -398,18 +398,28 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         }
         tmem_ld_wait();
         if constexpr (MOD) {
-          scale_scores(sm, sv);
-          if (sm.bias) {   // the list's gap, if the tile holds it: slots lie `shift` further behind key `gap`
-            const int gap = it.kl.cut - xt;
-            const float near = static_cast<float>(i - xt), far = static_cast<float>(i - xt - it.kl.shift);
-            if (gap <= 0 || gap >= kTcKeys) {
-              const float base = gap <= 0 ? far : near;
+          const int gap = it.kl.cut - xt;   // the list's gap, if the tile holds it: slots lie `shift` further behind it
+          const int near = i - xt, far = near - it.kl.shift;
+          const bool split = gap > 0 && gap < kTcKeys;
+          const int base = gap <= 0 ? far : near;
+          if (sm.cap2 > 0.f || !sm.bias) scale_scores(sm, sv);
+          if (sm.bias && !split && base >= kTcKeys - 1) {
+            // All keys before the row: - slope (base - e) is linear in e, two keys at a time.
+            const float b0 = -slope2 * static_cast<float>(base);
+            const uint64_t sl = f2_pack(slope2, slope2), bb = f2_pack(b0, b0);
+            const float one = sm.cap2 > 0.f ? 1.f : sm.sl2;
+            const uint64_t k2 = f2_pack(one, one);
 #pragma unroll
-              for (int e = 0; e < 128; ++e) sv[e] = fmaf(-slope2, fabsf(base - e), sv[e]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 128; ++e) sv[e] = fmaf(-slope2, fabsf((e >= gap ? far : near) - e), sv[e]);
+            for (int e = 0; e < 128; e += 2) {
+              const uint64_t bias = ffma2(f2_pack(e, e + 1), sl, bb);
+              f2_unpack(ffma2(f2_pack(sv[e], sv[e + 1]), k2, bias), sv[e], sv[e + 1]);
             }
+          } else if (sm.bias) {
+            const float one = sm.cap2 > 0.f ? 1.f : sm.sl2;
+            const float fn = static_cast<float>(split ? near : base), ff = static_cast<float>(split ? far : base);
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              sv[e] = fmaf(-slope2, fabsf((e >= gap ? ff : fn) - e), sv[e] * one);
           }
         }
         if (!((xt >= all_lo && xt + kTcKeys - 1 <= all_hi) || xt + kTcKeys - 1 < pre)) {

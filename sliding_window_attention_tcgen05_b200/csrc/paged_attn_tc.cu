@@ -68,6 +68,31 @@ __device__ __forceinline__ TcTiles tc_tiles(const PagedAttnArgs& a, const TcItem
   return t;
 }
 
+// Rows of tile u that the product with V reads: those of the list, rounded up
+// to the 16 of a product.
+__device__ __forceinline__ int tc_rows(const TcItem& it, int u) {
+  return (min(kTcKeys, it.x1 - it.x0 - u * kTcKeys) + 15) & ~15;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// 32 columns of O (zeros where no product was issued).
+__device__ __forceinline__ void tc_output(uint32_t addr, bool any, uint32_t (&o)[32]) {
+  if (any) {
+    tmem_ld32(addr, o);
+    tmem_ld_wait();
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = 0u;
+  }
+}
+
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {   // does not wait
   uint32_t ok;
   asm volatile(
@@ -142,6 +167,24 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     it.x1 = min(it.x0 + step, it.kl.total);
     it.nt = (it.x1 - it.x0 + kTcKeys - 1) / kTcKeys;
   }
+  // Pool rows of four rows of tile u, or -1: lane * 4 + k where runs are fetched
+  // by TMA (so that a run's rows are R / 4 neighbouring lanes'), else lane + 32 k.
+  const bool tma = run >= 16;
+  auto lookup = [&](int u, int (&row)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = it.x0 + u * kTcKeys + (tma ? lane * 4 + k : lane + 32 * k);
+      row[k] = -1;
+      if (u >= it.nt || x >= it.x1) continue;
+      const int j = key_slot(it.kl, x);
+      if (!wanted(it.kl, j)) continue;
+      row[k] = slot_row(a.c, it.s, it.kh, j);
+      if (row[k] < 0) report_bad_cache(a.status, it.s);
+    }
+  };
+  int next[4];
+  if (warp >= 10) lookup(0, next);   // its table reads travel under the set-up
+
   if (threadIdx.x == 0) {
     if (it.q.over) report_bad_cache(a.status, it.s);
     for (int i = 0; i < NST; ++i) { mbar_init(bar(FULL + i), 32); mbar_init(bar(EMPTY + i), it.n_act); }
@@ -153,7 +196,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       mbar_init(bar(DR + X), 1);
       mbar_init(bar(TK + X), 1);
     }
-    mbar_init(bar(QF), 64);
+    mbar_init(bar(QF), 128 * it.n_act);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -171,50 +214,20 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
     if (warp >= 10) {
-      // ------------- producers: half of Q each, then warp 10 the K and warp 11 the V tiles
+      // ------------- producers: warp 10 the K and warp 11 the V tiles
       constexpr int CPR = D / 8, RPI = 32 / CPR;      // 16-byte chunks of a row, rows per warp-wide copy
       const int c = lane % CPR, ch = c & 7, rl0 = lane / CPR;
       const uint32_t coff = (c >> 3) * (kTcKeys * 128);
       const bool is_v = warp == 11;
       const CUtensorMap* tm = is_v ? &tmV : &tmK;
-      const uint16_t* qp = static_cast<const uint16_t*>(a.q.p);
       const uint8_t* pool = static_cast<const uint8_t*>(is_v ? a.v : a.k) + c * 16;
       if (lane == 0) tma_prefetch_desc(tm);
-      for (int X = 0; X < it.n_act; ++X) {
-        const uint32_t dst = smem_addr(sQ + X * TILE) + coff;
-        for (int k = 0; k < 64 / RPI; ++k) {
-          const int r = (is_v ? 64 : 0) + k * RPI + rl0;
-          const int rr = it.r0 + X * 128 + r;
-          const bool ok = rr < it.rows;
-          const int t = a.group_div.div(ok ? rr : 0), h = it.kh * a.group + (ok ? rr : 0) - t * a.group;
-          cp_async16(dst + r * 128 + ((ch ^ (r & 7)) << 4),
-                     qp + (it.q.row0 + t) * a.q.row + h * a.q.head + c * 8, ok);
-        }
-      }
-      cp_async_commit();
-      // Pool rows of four rows of tile u, or -1: lane * 4 + k where runs are fetched
-      // by TMA (so that a run's rows are R / 4 neighbouring lanes'), else lane + 32 k.
-      const bool tma = run >= 16;
-      auto lookup = [&](int u, int (&row)[4]) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int x = it.x0 + u * kTcKeys + (tma ? lane * 4 + k : lane + 32 * k);
-          row[k] = -1;
-          if (u >= it.nt || x >= it.x1) continue;
-          const int j = key_slot(it.kl, x);
-          if (!wanted(it.kl, j)) continue;
-          row[k] = slot_row(a.c, it.s, it.kh, j);
-          if (row[k] < 0) report_bad_cache(a.status, it.s);
-        }
-      };
-      int row[4], next[4];
-      lookup(0, next);
+      int row[4];
       int u = 0, told = 0;   // tiles issued, tiles whose arrival the consumers were told of (cp.async)
       auto stage_of = [&](int v) { return (2 * v + (is_v ? 1 : 0)) % NST; };
-      auto landed = [&](int in_flight) {   // tile `told` (and Q before it) has landed once so many newer ones fly
+      auto landed = [&](int in_flight) {   // tile `told` has landed once so many newer ones fly
         if (in_flight >= 1) cp_async_wait<1>(); else cp_async_wait<0>();
         fence_proxy_async_smem();
-        if (told == 0) mbar_arrive(bar(QF));
         mbar_arrive(bar(FULL + stage_of(told)));
         ++told;
       };
@@ -224,7 +237,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         const uint32_t empty = (((2 * u + (is_v ? 1 : 0)) / NST) & 1) ^ 1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) row[k] = next[k];
-        lookup(u + 1, next);
+        const int used = tc_rows(it, u);   // rows that the product with V reads
         // No free buffer: nothing to issue, so pass on what lands meanwhile.
         if (!tma)
           while (told < u && !__all_sync(0xffffffffu, mbar_test_wait(bar(EMPTY + st), empty))) landed(u - told - 1);
@@ -242,8 +255,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
             for (int hf = 0; hf < D / 64; ++hf)
               tma_load_2d(dst + hf * (kTcKeys * 128) + lane * 512, tm, full, hf * 64, row[0]);
-          if (runs != 0xffffffffu) {
-            for (int k = 0; k < 128 / RPI; ++k) {
+          if (runs != 0xffffffffu) {   // rows of runs that hold others than the block's keys, zeros for those
+            for (int k = 0; k < used / RPI; ++k) {
               const int r = k * RPI + rl0;
               if ((runs >> (k * RPI / 4)) & 1u) continue;              // a warp-wide copy lies in one run
               int gr = -1;
@@ -260,14 +273,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
             fence_proxy_async_smem();
           }
           if (lane != 0) mbar_arrive(full);
-          if (u == 0) {   // Q, copied before the first tile
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
-            mbar_arrive(bar(QF));
-          }
         } else {
 #pragma unroll
           for (int k0 = 0; k0 < 128 / RPI; k0 += 8) {   // eight rows' numbers first: a shuffle before each copy takes 75 cycles a copy
+            if (k0 * RPI >= used) break;
             int gr[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -282,6 +291,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           cp_async_commit();
           if (u - told >= Cfg::kLag) landed(Cfg::kLag);
         }
+        lookup(u + 1, next);
       }
       while (!tma && u == it.nt && told < u) landed(u - told - 1);
       cp_async_wait<0>();
@@ -312,11 +322,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         const int bk = 2 * u + 2, bv = 2 * u + 1, sk = bk % NST, sv = bv % NST, t = u - tiles.first;
         const bool pv = u >= tiles.first && u < tiles.end, sc = u + 1 >= tiles.first && u + 1 < tiles.end;
         const uint64_t dv = desc_v + static_cast<uint32_t>(sv * (TILE >> 4));
+        const int used = tc_rows(it, u);
         auto half_pv = [&](int half) {
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {   // 16 keys: 8 TMEM columns of P, 16 rows of V
             const int kk = half * 4 + k4;
-            umma_bf16_ts(tO, tS + 8 * kk, dv + kk * (2048 >> 4), idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
+            if (kk * 16 < used) umma_bf16_ts(tO, tS + 8 * kk, dv + kk * (2048 >> 4), idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
           }
         };
         if (u >= 0 && !(ok = mbar_wait(bar(FULL + sv), (bv / NST) & 1, wc, 73))) break;
@@ -367,6 +378,23 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     // ------------- softmax: warpgroup X, thread = row
     const int X = warp >> 2;
     if (X < it.n_act) {
+      {   // Q: the warp's 32 rows (those past the sequence's as zeros)
+        constexpr int CPR = D / 8, RPI = 32 / CPR;
+        const int c = lane % CPR;
+        const uint32_t dst = smem_addr(sQ + X * TILE) + (c >> 3) * (kTcKeys * 128);
+#pragma unroll
+        for (int k = 0; k < 32 / RPI; ++k) {
+          const int rl = (warp & 3) * 32 + k * RPI + lane / CPR, rr = it.r0 + X * 128 + rl;
+          const bool ok = rr < it.rows;
+          const int t = a.group_div.div(ok ? rr : 0), h = it.kh * a.group + (ok ? rr : 0) - t * a.group;
+          cp_async16(dst + rl * 128 + (((c & 7) ^ (rl & 7)) << 4),
+                     static_cast<const uint16_t*>(a.q.p) + (it.q.row0 + t) * a.q.row + h * a.q.head + c * 8, ok);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        mbar_arrive(bar(QF));
+      }
       const int r = it.r0 + X * 128 + (threadIdx.x & 127);
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tS = tmem + X * 128 + lane_off, tO = tmem + 256 + X * D + lane_off;
@@ -492,40 +520,61 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         tc_fence_after();
       }
       if (ok) {
-        const int64_t tok = it.q.row0 + tt;
-        const bool mine = r < it.rows;
+        // Rows go out through 4 KB of the warpgroup's Q tile (its products have read it) so that eight lanes write 128
+        // bytes of a row: chunk g of row r at r * 128 + ((g ^ (r & 7)) << 4).
         const bool empty = l_run == 0.f;   // a NaN score leaves a NaN sum
         const float inv = empty ? 0.f : 1.f / l_run;
-        const int64_t pr = (static_cast<int64_t>(it.sp) * a.ch.n_tokens + tok) * a.n_q_heads + h;
+        const uint32_t stage = smem_addr(sQ + X * TILE) + (warp & 3) * 4096;
+        const int rl = lane >> 3, g = lane & 7;
+        int64_t at[8];   // of rows 4 k + rl: the row of the partial results, or the element of o; -1 past the sequence
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (t > 0) {
-            tmem_ld32(tO + 32 * c, o);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
-          }
-          if (!mine) continue;
-          if (a.parts > 1) {
-            float* dst = a.part_o + pr * D + c * 32;
-            if (!empty)
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) st_global_v4(dst + e, o[e], o[e + 1], o[e + 2], o[e + 3]);
-          } else {
-            uint16_t* dst = static_cast<uint16_t*>(a.o) + tok * a.o_row + h * a.o_head + c * 32;
-            uint32_t y[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              y[e] = empty ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) st_global_v4(dst + 2 * e, y[e], y[e + 1], y[e + 2], y[e + 3]);
-          }
+        for (int k = 0; k < 8; ++k) {
+          const int ro = it.r0 + X * 128 + (warp & 3) * 32 + 4 * k + rl;
+          const int to = a.group_div.div(min(ro, it.rows - 1)), ho = it.kh * a.group + min(ro, it.rows - 1) - to * a.group;
+          const int64_t tok = it.q.row0 + to;
+          at[k] = ro >= it.rows ? -1
+                  : a.parts > 1 ? (static_cast<int64_t>(it.sp) * a.ch.n_tokens + tok) * a.n_q_heads + ho
+                                : tok * a.o_row + ho * a.o_head;
         }
-        if (mine) {
-          if (a.parts > 1) a.part_ml[pr] = make_float2(m_used, l_run);
-          else if (a.lse) a.lse[tok * a.n_q_heads + h] = empty ? -INFINITY : (m_used + log2f(l_run)) * kLn2;
+        constexpr int kWide = D / 32;   // 32-column chunks
+        const int words = a.parts > 1 ? 1 : 2;   // columns of a staged word
+        for (int c = 0; c < kWide; c += words) {
+          uint32_t w[32];
+          if (words == 1) {
+            tc_output(tO + 32 * c, t > 0, w);
+          } else {
+            uint32_t o[32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              tc_output(tO + 32 * (c + half), t > 0, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                w[16 * half + e] =
+                    empty ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            st_shared_v4(stage + lane * 128 + ((k ^ (lane & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 4 * k + rl;
+            const uint4 y = ld_shared_v4(stage + rr * 128 + ((g ^ (rr & 7)) << 4));
+            if (at[k] < 0) continue;
+            if (words == 1)
+              st_global_v4(a.part_o + at[k] * D + c * 32 + g * 4, y.x, y.y, y.z, y.w);
+            else
+              st_global_v4(static_cast<uint16_t*>(a.o) + at[k] + c * 32 + g * 8, y.x, y.y, y.z, y.w);
+          }
+          __syncwarp();
+        }
+        if (r < it.rows) {
+          const int64_t tok = it.q.row0 + tt;
+          if (a.parts > 1)
+            a.part_ml[(static_cast<int64_t>(it.sp) * a.ch.n_tokens + tok) * a.n_q_heads + h] = make_float2(m_used, l_run);
+          else if (a.lse)
+            a.lse[tok * a.n_q_heads + h] = empty ? -INFINITY : (m_used + log2f(l_run)) * kLn2;
         }
       }
       tc_fence_before();

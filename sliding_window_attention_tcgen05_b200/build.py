@@ -8,6 +8,9 @@
 Each csrc/*.cu is compiled to _build/<name>.o (rebuilt when it or any header
 is newer than its object) and the objects are linked into
 sliding_window_attention_tcgen05_b200/libvx.so with a static CUDA runtime.
+csrc/bind.cpp (the paged-cache wrappers' marshalling, against PyTorch's C++
+headers) becomes sliding_window_attention_tcgen05_b200/_bind.so, which calls
+into libvx.so.
 """
 from __future__ import annotations
 
@@ -24,6 +27,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvx.so")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
@@ -88,7 +92,34 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         p = subprocess.run(cmd, capture_output=True, text=True)
         if p.returncode != 0:
             raise RuntimeError("link failed:\n" + p.stdout + p.stderr)
+    build_bind(force=force, verbose=verbose)
     return LIB
+
+
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    """_bind.so; needs libvx.so."""
+    src = os.path.join(CSRC, "bind.cpp")
+    hdr = os.path.getmtime(os.path.join(ROOT, "include", "vx.h"))
+    if not force and not _stale(src, BIND, hdr):
+        return BIND
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_bind",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, src, "-o", BIND, "-L", lib, "-L", PKG,
+           "-l:libvx.so", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError("bind.cpp failed:\n" + p.stdout + p.stderr)
+    return BIND
 
 
 def main(argv=None):

@@ -27,7 +27,7 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
     const int block = f32_block_rows(rows);
     ctas = lanes * ((rows + block - 1) / block);
     want = block == 64 ? 2 * kPlanSms : 6 * kPlanSms;
-    min_keys = 128;
+    min_keys = block == 8 ? 64 : 128;
   } else if (rows <= 32) {
     // A row block of the tcgen05 kernel would be at least three quarters padding.
     p.kernel = 0;
@@ -67,7 +67,7 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
   p.w_segs = static_cast<int>(segs < 1 ? 1 : segs);
   // Up to 8 rows: their scores, 4 bytes a key each, against another read of K (2 * head_dim bytes a key); not where
   // the tables' length would ask for a workspace of hundreds of megabytes.
-  p.keep_scores = p.kernel == 0 && rows <= 8 && lanes * rows * max_kv * 4 <= (256ll << 20);
+  p.keep_scores = (p.kernel == 0 || p.kernel == 2) && rows <= 8 && lanes * rows * max_kv * 4 <= (256ll << 20);
   return p;
 }
 
@@ -428,7 +428,7 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
   a.status = L.status;
   a.limit_ns = L.limit_ns;
   const int64_t rows = static_cast<int64_t>(mq) * group;
-  const int64_t blocks = plan.kernel == 1 ? (rows + 255) / 256 : plan.kernel == 2 ? (rows + 15) / 16 : 1;
+  const int64_t blocks = plan.kernel == 1 ? (rows + 255) / 256 : plan.kernel == 2 ? (rows + 7) / 8 : 1;
   VX_CHECK_ARG(blocks * cache->n_seqs * cache->n_kv_heads * plan.splits < INT_MAX, "%s: too many row blocks", what);
   VX_CUDA(traced(L, plan.kernel == 0 ? "paged_attn_rows" : plan.kernel == 1 ? "paged_attn_tc" : "paged_attn_f32", 1, [&] {
     return plan.kernel == 0   ? launch_paged_attn_rows(L, a)

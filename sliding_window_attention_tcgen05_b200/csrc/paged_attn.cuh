@@ -138,7 +138,9 @@ cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, b
 
 constexpr int kMaxSplits = 64;
 
-// Rows of a block of the fp32 kernel, for sequences of up to `rows` rows.
-inline int f32_block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Rows of a block of the fp32 kernels, for sequences of up to `rows` rows: 8 is
+// the kernel for few rows (twice over the keys for 9 to 16, from L2), 32 and
+// 64 the tiled one.
+inline int f32_block_rows(int64_t rows) { return rows <= 16 ? 8 : rows <= 32 ? 32 : 64; }
 
 }  // namespace vx

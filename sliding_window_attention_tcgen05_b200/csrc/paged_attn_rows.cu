@@ -357,9 +357,8 @@ paged_attn_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
 // sequence), CUDA cores throughout (tensor-core tf32 would keep 10 mantissa
 // bits).  256 threads as 16 x 16: a thread computes RM rows x 4 keys of a
 // 64-key tile's scores and RM rows x D / 16 dims of the output, so that shared
-// memory is read once for 8 (RM 4) or 4 multiply-adds; the V tile travels
-// while the scores are computed and the next K tile while P V is.  RM follows
-// the number of rows; at RM 1 the shared-memory reads bound it.
+// memory is read once for 8 (RM 4) or 5 multiply-adds; the V tile travels
+// while the scores are computed and the next K tile while P V is.
 constexpr int kF32Threads = 256;
 constexpr int kF32Keys = 64;
 
@@ -544,6 +543,183 @@ __global__ void __launch_bounds__(kF32Threads) paged_attn_f32_kernel(const __gri
     for (int e = 0; e < DV; ++e)
       *reinterpret_cast<float4*>(dst + tx * 4 + 64 * e) =
           make_float4(o[i][4 * e] * inv, o[i][4 * e + 1] * inv, o[i][4 * e + 2] * inv, o[i][4 * e + 3] * inv);
+  }
+}
+
+// paged_attn_f32_rows_kernel: the fp32 form for few rows.  CTA per (block of 8
+// rows x key range, K/V head, sequence), four warps.  D / 8 lanes share a key
+// (8 dims each): K and V go straight from global memory to registers, one step
+// ahead, and meet the 8 rows' queries and outputs there, so shared memory is
+// only used to join the warps.  The dot products' partial sums are added by an
+// exchange that leaves row r's score in lane r of the key's lanes.
+constexpr int kF32RowBlock = 8;
+
+template <int D>
+__global__ void __launch_bounds__(128) paged_attn_f32_rows_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int R = kF32RowBlock, LPK = D / 8, KPW = 32 / LPK;   // lanes of a key, keys of a warp's step
+  constexpr int STEP = 4 * KPW;                                  // keys of the CTA's step
+  __shared__ float sm_m[4][R], sm_l[4][R];
+  __shared__ __align__(16) float sm_o[4][R][D];
+  const int rb = blockIdx.x % blocks, sp = blockIdx.x / blocks, kh = blockIdx.y, s = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / LPK, e = lane % LPK, rl = lane & 7;
+  const SeqSpan q = seq_span(a.c, a.ch, s);
+  const int G = a.group, rows = q.n * G, r0 = rb * R;
+  if (r0 >= rows) return;
+  if (q.over && threadIdx.x == 0) report_bad_cache(a.status, s);
+  const int rn = min(R, rows - r0);
+  const int tf = a.group_div.div(r0), tl = a.group_div.div(r0 + rn - 1);
+  const KeyList kl = key_list(q.old + tf, q.old + tl, a.window, a.prefix ? a.prefix[s] : 0, q.kv);
+  const int step = ((kl.total + a.splits - 1) / a.splits + STEP - 1) / STEP * STEP;
+  const int x0 = min(sp * step, kl.total), x1 = min(x0 + step, kl.total);
+  const int steps = (x1 - x0 + STEP - 1) / STEP;
+  const float* kp = static_cast<const float*>(a.k) + e * 4;
+  const float* vp = static_cast<const float*>(a.v) + e * 4;
+  float4 k0, k1, v0, v1;
+  auto fetch = [&](int i) {   // dims 4 e .. and D / 2 + 4 e .. of this lane's key of step i
+    k0 = k1 = v0 = v1 = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int x = x0 + i * STEP + warp * KPW + g;
+    if (i >= steps || x >= x1) return;
+    const int row = slot_row(a.c, s, kh, key_slot(kl, x));
+    if (row < 0) {
+      report_bad_cache(a.status, s);
+      return;
+    }
+    const int64_t at = static_cast<int64_t>(row) * D;
+    k0 = *reinterpret_cast<const float4*>(kp + at);
+    k1 = *reinterpret_cast<const float4*>(kp + at + D / 2);
+    v0 = *reinterpret_cast<const float4*>(vp + at);
+    v1 = *reinterpret_cast<const float4*>(vp + at + D / 2);
+  };
+  fetch(0);
+  float qr[R][8], o[R][8];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int rr = min(r0 + r, rows - 1);
+    const int t = a.group_div.div(rr), h = kh * G + rr - t * G;
+    const float* src = static_cast<const float*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head + e * 4;
+    const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + D / 2);
+    qr[r][0] = x.x; qr[r][1] = x.y; qr[r][2] = x.z; qr[r][3] = x.w;
+    qr[r][4] = y.x; qr[r][5] = y.y; qr[r][6] = y.z; qr[r][7] = y.w;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) o[r][d] = 0.f;
+  }
+  // This lane's row of the scores.
+  const ScoreMod sm = score_mod(a);
+  const int mr = min(r0 + rl, rows - 1), mt = a.group_div.div(mr), mi = q.old + mt;
+  const float slope2 = a.slopes ? a.slopes[kh * G + mr - mt * G] * kLog2e : 0.f;
+  float* kept = nullptr;
+  if (a.scores != nullptr && rl < rn && e < 8)
+    kept = a.scores + ((static_cast<int64_t>(s) * a.c.n_heads + kh) * (a.ch.max_q * G) + r0 + rl) * a.score_stride;
+  float m = -INFINITY, l = 0.f;
+  for (int i = 0; i < steps; ++i) {
+    const float kk[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+    const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    fetch(i + 1);
+    float dot[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      dot[r] = 0.f;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) dot[r] = fmaf(qr[r][d], kk[d], dot[r]);
+    }
+    if constexpr (LPK == 16) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], 8);
+    }
+    // Halve the rows and the lanes that share them, three times: lane rl ends with row rl.
+#pragma unroll
+    for (int w = 4; w > 0; w >>= 1) {
+      const bool up = (lane & w) != 0;
+#pragma unroll
+      for (int r = 0; r < w; ++r) {
+        const float keep = up ? dot[r + w] : dot[r], give = up ? dot[r] : dot[r + w];
+        dot[r] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+      }
+    }
+    const int x = x0 + i * STEP + warp * KPW + g, j = key_slot(kl, x);
+    const bool seen = x < x1 && (j < kl.pre || (j <= mi && j > mi - a.window));
+    const float y = seen ? score2(sm, dot[0], slope2, mi - j) : -INFINITY;
+    if (kept != nullptr && x < a.score_stride) kept[x] = y;
+    float cmax = y;
+#pragma unroll
+    for (int off = LPK; off < 32; off <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, off));
+    const bool grew = cmax > m + kRowsSlack;
+    float alpha = 1.f;
+    if (grew) {
+      alpha = exp2f(m - cmax);   // 0 for the first keys
+      m = cmax;
+    }
+    if (__any_sync(0xffffffffu, grew)) {
+      l *= alpha;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float f = __shfl_sync(0xffffffffu, alpha, (lane & -LPK) | r);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[r][d] *= f;
+      }
+    }
+    const float p = exp2f(y - (m == -INFINITY ? 0.f : m));
+    l += p;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float f = __shfl_sync(0xffffffffu, p, (lane & -LPK) | r);
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[r][d] = fmaf(f, vv[d], o[r][d]);
+    }
+  }
+  // Join the warp's keys, then the warps.
+#pragma unroll
+  for (int off = LPK; off < 32; off <<= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[r][d] += __shfl_xor_sync(0xffffffffu, o[r][d], off);
+  }
+  if (lane < R) {
+    sm_m[warp][lane] = m;
+    sm_l[warp][lane] = l;
+  }
+  if (g == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      *reinterpret_cast<float4*>(&sm_o[warp][r][e * 4]) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+      *reinterpret_cast<float4*>(&sm_o[warp][r][D / 2 + e * 4]) = make_float4(o[r][4], o[r][5], o[r][6], o[r][7]);
+    }
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < rn * (D / 4); idx += 128) {
+    const int r = idx / (D / 4), d = idx % (D / 4) * 4;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w][r]);
+    float L = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (sm_l[w][r] == 0.f) continue;   // the warp saw no key (a NaN score leaves a NaN sum)
+      const float f = exp2f(sm_m[w][r] - M);
+      const float4 z = *reinterpret_cast<const float4*>(&sm_o[w][r][d]);
+      L = fmaf(sm_l[w][r], f, L);
+      y.x = fmaf(z.x, f, y.x);
+      y.y = fmaf(z.y, f, y.y);
+      y.z = fmaf(z.z, f, y.z);
+      y.w = fmaf(z.w, f, y.w);
+    }
+    const int t = a.group_div.div(r0 + r), h = kh * G + r0 + r - t * G;
+    const int64_t tok = q.row0 + t;
+    if (a.parts > 1) {
+      const int64_t pr = (static_cast<int64_t>(sp) * a.ch.n_tokens + tok) * a.n_q_heads + h;
+      *reinterpret_cast<float4*>(a.part_o + pr * D + d) = y;
+      if (d == 0) a.part_ml[pr] = make_float2(M, L);
+    } else {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      *reinterpret_cast<float4*>(static_cast<float*>(a.o) + tok * a.o_row + h * a.o_head + d) =
+          make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      if (d == 0 && a.lse) a.lse[tok * a.n_q_heads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
   }
 }
 
@@ -815,7 +991,7 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
 // The same sum from the scores that the rows kernel kept (base 2, by list
 // position; up to 8 rows, so that writing and reading them costs less than
 // reading K again).  A thread per slot.
-template <int D>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(256) paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -841,13 +1017,15 @@ __global__ void __launch_bounds__(256) paged_attn_weights_kept_kernel(const __gr
         for (int r = 0; r < rows; ++r) sum += ex2_approx(kept[r * a.score_stride + x] - s_lse[r]);
       } else if (row >= 0) {   // the caller's max_kv was too low: the product again
         const ScoreMod sm = score_mod(a);
-        const uint16_t* k = static_cast<const uint16_t*>(a.k) + static_cast<int64_t>(row) * D;
         for (int r = 0; r < rows; ++r) {
           const int t = a.group_div.div(r), h = kh * G + r - t * G, i = q.old + t;
           if (!(j < kl.pre || (j <= i && j > i - a.window))) continue;
-          const uint16_t* qp = static_cast<const uint16_t*>(a.q.p) + (q.row0 + t) * a.q.row + h * a.q.head;
+          const int64_t qe = (q.row0 + t) * a.q.row + h * a.q.head, ke = static_cast<int64_t>(row) * D;
           float dot = 0.f;
-          for (int d = 0; d < D; ++d) dot = fmaf(bf16_to_f(qp[d]), bf16_to_f(k[d]), dot);
+          for (int d = 0; d < D; ++d)
+            dot = BF16 ? fmaf(bf16_to_f(static_cast<const uint16_t*>(a.q.p)[qe + d]),
+                              bf16_to_f(static_cast<const uint16_t*>(a.k)[ke + d]), dot)
+                       : fmaf(static_cast<const float*>(a.q.p)[qe + d], static_cast<const float*>(a.k)[ke + d], dot);
           sum += ex2_approx(score2(sm, dot, a.slopes ? a.slopes[h] * kLog2e : 0.f, i - j) - s_lse[r]);
         }
       }
@@ -1047,10 +1225,16 @@ cudaError_t launch_paged_attn_rows(const Launch& L, const PagedAttnArgs& a) {
 }
 
 cudaError_t launch_paged_attn_f32(const Launch& L, const PagedAttnArgs& a) {
-  const int rows = f32_block_rows(static_cast<int64_t>(a.ch.max_q) * a.group);
-  if (a.head_dim == 128)
-    return rows == 16 ? launch_f32<128, 1>(L, a) : rows == 32 ? launch_f32<128, 2>(L, a) : launch_f32<128, 4>(L, a);
-  return rows == 16 ? launch_f32<64, 1>(L, a) : rows == 32 ? launch_f32<64, 2>(L, a) : launch_f32<64, 4>(L, a);
+  const int64_t all = static_cast<int64_t>(a.ch.max_q) * a.group;
+  const int block = f32_block_rows(all);
+  if (block == kF32RowBlock) {
+    const int blocks = static_cast<int>((all + block - 1) / block);
+    const dim3 grid(static_cast<unsigned>(blocks) * a.splits, a.c.n_heads, a.c.n_seqs);
+    return a.head_dim == 128 ? launch_kernel(paged_attn_f32_rows_kernel<128>, grid, dim3(128), 0, L.stream, a, blocks)
+                             : launch_kernel(paged_attn_f32_rows_kernel<64>, grid, dim3(128), 0, L.stream, a, blocks);
+  }
+  if (a.head_dim == 128) return block == 32 ? launch_f32<128, 2>(L, a) : launch_f32<128, 4>(L, a);
+  return block == 32 ? launch_f32<64, 2>(L, a) : launch_f32<64, 4>(L, a);
 }
 
 cudaError_t launch_paged_attn_combine(const Launch& L, const PagedAttnArgs& a, bool bf16) {
@@ -1062,8 +1246,11 @@ cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, b
   const bool mod = a.cap > 0.f || a.slopes != nullptr;
   if (a.scores != nullptr) {
     const dim3 g(static_cast<unsigned>((max_kv + 255) / 256), a.c.n_heads, a.c.n_seqs);
-    return a.head_dim == 128 ? launch_kernel(paged_attn_weights_kept_kernel<128>, g, dim3(256), 0, L.stream, a)
-                             : launch_kernel(paged_attn_weights_kept_kernel<64>, g, dim3(256), 0, L.stream, a);
+    if (a.head_dim == 128)
+      return bf16 ? launch_kernel(paged_attn_weights_kept_kernel<128, true>, g, dim3(256), 0, L.stream, a)
+                  : launch_kernel(paged_attn_weights_kept_kernel<128, false>, g, dim3(256), 0, L.stream, a);
+    return bf16 ? launch_kernel(paged_attn_weights_kept_kernel<64, true>, g, dim3(256), 0, L.stream, a)
+                : launch_kernel(paged_attn_weights_kept_kernel<64, false>, g, dim3(256), 0, L.stream, a);
   }
   const int keys = bf16 ? kWKeys : kWKeysF32;
   const dim3 grid(static_cast<unsigned>((max_kv + keys - 1) / keys * a.w_segs), a.c.n_heads, a.c.n_seqs);

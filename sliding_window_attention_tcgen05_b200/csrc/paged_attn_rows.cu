@@ -548,20 +548,25 @@ __global__ void __launch_bounds__(kF32Threads) paged_attn_f32_kernel(const __gri
 
 // paged_attn_f32_rows_kernel: the fp32 form for few rows.  CTA per (block of 8
 // rows x key range, K/V head, sequence), four warps.  D / 8 lanes share a key
-// (8 dims each): K and V go straight from global memory to registers, one step
-// ahead, and meet the 8 rows' queries and outputs there, so shared memory is
-// only used to join the warps.  The dot products' partial sums are added by an
+// (8 dims each), which holds the 8 rows' queries and outputs of its dims in
+// registers.  Each lane copies its own piece of K and V through a ring of
+// cp.async stages in shared memory, several steps ahead.  The dot products' partial sums are added by an
 // exchange that leaves row r's score in lane r of the key's lanes.
 constexpr int kF32RowBlock = 8;
+constexpr int kF32RowStages = 3;
+constexpr int kF32RowDeep = 2;   // keys of a lane's step: two chains of shuffles and exponentials in flight
+constexpr size_t kF32RowSmem = 128 * kF32RowStages * kF32RowDeep * 64;   // a lane's 64 bytes of a key
 
 template <int D>
 __global__ void __launch_bounds__(128) paged_attn_f32_rows_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
   pdl_wait();
   pdl_trigger();
   constexpr int R = kF32RowBlock, LPK = D / 8, KPW = 32 / LPK;   // lanes of a key, keys of a warp's step
-  constexpr int STEP = 4 * KPW;                                  // keys of the CTA's step
-  __shared__ float sm_m[4][R], sm_l[4][R];
-  __shared__ __align__(16) float sm_o[4][R][D];
+  constexpr int U = kF32RowDeep, WARP = U * KPW, STEP = 4 * WARP;   // keys of a warp's step and of the CTA's
+  extern __shared__ __align__(16) float fsm[];
+  float(*sm_m)[R] = reinterpret_cast<float(*)[R]>(fsm);                 // [4][R]: these once the ring is done
+  float(*sm_l)[R] = sm_m + 4;                                           // [4][R]
+  float(*sm_o)[R][D] = reinterpret_cast<float(*)[R][D]>(fsm + 8 * R);   // [4][R][D]
   const int rb = blockIdx.x % blocks, sp = blockIdx.x / blocks, kh = blockIdx.y, s = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / LPK, e = lane % LPK, rl = lane & 7;
   const SeqSpan q = seq_span(a.c, a.ch, s);
@@ -576,23 +581,40 @@ __global__ void __launch_bounds__(128) paged_attn_f32_rows_kernel(const __grid_c
   const int steps = (x1 - x0 + STEP - 1) / STEP;
   const float* kp = static_cast<const float*>(a.k) + e * 4;
   const float* vp = static_cast<const float*>(a.v) + e * 4;
-  float4 k0, k1, v0, v1;
-  auto fetch = [&](int i) {   // dims 4 e .. and D / 2 + 4 e .. of this lane's key of step i
-    k0 = k1 = v0 = v1 = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int x = x0 + i * STEP + warp * KPW + g;
-    if (i >= steps || x >= x1) return;
-    const int row = slot_row(a.c, s, kh, key_slot(kl, x));
-    if (row < 0) {
-      report_bad_cache(a.status, s);
-      return;
+  auto key_of = [&](int i, int u) { return x0 + i * STEP + warp * WARP + u * KPW + g; };   // this lane's, in the list
+  auto lookup = [&](int i, int (&row)[U]) {   // their pool rows, or -1
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = key_of(i, u);
+      row[u] = -1;
+      if (i >= steps || x >= x1) continue;
+      row[u] = slot_row(a.c, s, kh, key_slot(kl, x));
+      if (row[u] < 0) report_bad_cache(a.status, s);
     }
-    const int64_t at = static_cast<int64_t>(row) * D;
-    k0 = *reinterpret_cast<const float4*>(kp + at);
-    k1 = *reinterpret_cast<const float4*>(kp + at + D / 2);
-    v0 = *reinterpret_cast<const float4*>(vp + at);
-    v1 = *reinterpret_cast<const float4*>(vp + at + D / 2);
   };
-  fetch(0);
+  // Of each key, 4 x (32 lanes x 16 bytes): K dims 4 e .., K dims D / 2 + 4 e .., then V's.
+  const uint32_t ring = smem_addr(fsm) + warp * (kF32RowStages * U * 2048) + lane * 16;
+  auto fetch = [&](int i, const int (&row)[U]) {
+    if (i < steps) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t dst = ring + (i % kF32RowStages * U + u) * 2048;
+        const int64_t at = static_cast<int64_t>(max(row[u], 0)) * D;
+        cp_async16(dst, kp + at, row[u] >= 0);
+        cp_async16(dst + 512, kp + at + D / 2, row[u] >= 0);
+        cp_async16(dst + 1024, vp + at, row[u] >= 0);
+        cp_async16(dst + 1536, vp + at + D / 2, row[u] >= 0);
+      }
+    }
+    cp_async_commit();
+  };
+  int next_row[U];
+#pragma unroll
+  for (int i = 0; i < kF32RowStages - 1; ++i) {
+    lookup(i, next_row);
+    fetch(i, next_row);
+  }
+  lookup(kF32RowStages - 1, next_row);
   float qr[R][8], o[R][8];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -614,35 +636,53 @@ __global__ void __launch_bounds__(128) paged_attn_f32_rows_kernel(const __grid_c
     kept = a.scores + ((static_cast<int64_t>(s) * a.c.n_heads + kh) * (a.ch.max_q * G) + r0 + rl) * a.score_stride;
   float m = -INFINITY, l = 0.f;
   for (int i = 0; i < steps; ++i) {
-    const float kk[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-    const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    fetch(i + 1);
-    float dot[R];
+    cp_async_wait<kF32RowStages - 2>();
+    const float* st = fsm + (warp * kF32RowStages + i % kF32RowStages) * (U * 512) + lane * 4;   // what this lane copied
+    float dot[U][R], v[U][8];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      dot[r] = 0.f;
+    for (int u = 0; u < U; ++u) {
+      float k[8];
 #pragma unroll
-      for (int d = 0; d < 8; ++d) dot[r] = fmaf(qr[r][d], kk[d], dot[r]);
+      for (int c = 0; c < 2; ++c) {
+        *reinterpret_cast<float4*>(k + 4 * c) = *reinterpret_cast<const float4*>(st + u * 512 + c * 128);
+        *reinterpret_cast<float4*>(v[u] + 4 * c) = *reinterpret_cast<const float4*>(st + u * 512 + 256 + c * 128);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        dot[u][r] = 0.f;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) dot[u][r] = fmaf(qr[r][d], k[d], dot[u][r]);
+      }
     }
+    fetch(i + kF32RowStages - 1, next_row);   // into the stage of the last step
+    lookup(i + kF32RowStages, next_row);
     if constexpr (LPK == 16) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], 8);
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < R; ++r) dot[u][r] += __shfl_xor_sync(0xffffffffu, dot[u][r], 8);
     }
     // Halve the rows and the lanes that share them, three times: lane rl ends with row rl.
 #pragma unroll
     for (int w = 4; w > 0; w >>= 1) {
       const bool up = (lane & w) != 0;
 #pragma unroll
-      for (int r = 0; r < w; ++r) {
-        const float keep = up ? dot[r + w] : dot[r], give = up ? dot[r] : dot[r + w];
-        dot[r] = keep + __shfl_xor_sync(0xffffffffu, give, w);
-      }
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < w; ++r) {
+          const float keep = up ? dot[u][r + w] : dot[u][r], give = up ? dot[u][r] : dot[u][r + w];
+          dot[u][r] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        }
     }
-    const int x = x0 + i * STEP + warp * KPW + g, j = key_slot(kl, x);
-    const bool seen = x < x1 && (j < kl.pre || (j <= mi && j > mi - a.window));
-    const float y = seen ? score2(sm, dot[0], slope2, mi - j) : -INFINITY;
-    if (kept != nullptr && x < a.score_stride) kept[x] = y;
-    float cmax = y;
+    float y[U], cmax = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = key_of(i, u), j = key_slot(kl, x);
+      const bool seen = x < x1 && (j < kl.pre || (j <= mi && j > mi - a.window));
+      y[u] = seen ? score2(sm, dot[u][0], slope2, mi - j) : -INFINITY;
+      if (kept != nullptr && x < a.score_stride) kept[x] = y[u];
+      cmax = fmaxf(cmax, y[u]);
+    }
 #pragma unroll
     for (int off = LPK; off < 32; off <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, off));
     const bool grew = cmax > m + kRowsSlack;
@@ -660,15 +700,23 @@ __global__ void __launch_bounds__(128) paged_attn_f32_rows_kernel(const __grid_c
         for (int d = 0; d < 8; ++d) o[r][d] *= f;
       }
     }
-    const float p = exp2f(y - (m == -INFINITY ? 0.f : m));
-    l += p;
+    float p[U];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float f = __shfl_sync(0xffffffffu, p, (lane & -LPK) | r);
-#pragma unroll
-      for (int d = 0; d < 8; ++d) o[r][d] = fmaf(f, vv[d], o[r][d]);
+    for (int u = 0; u < U; ++u) {
+      p[u] = exp2f(y[u] - (m == -INFINITY ? 0.f : m));
+      l += p[u];
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = __shfl_sync(0xffffffffu, p[u], (lane & -LPK) | r);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[r][d] = fmaf(f, v[u][d], o[r][d]);
+      }
   }
+  cp_async_wait<0>();
+  __syncthreads();   // the ring becomes the join's
   // Join the warp's keys, then the warps.
 #pragma unroll
   for (int off = LPK; off < 32; off <<= 1) {
@@ -1230,8 +1278,8 @@ cudaError_t launch_paged_attn_f32(const Launch& L, const PagedAttnArgs& a) {
   if (block == kF32RowBlock) {
     const int blocks = static_cast<int>((all + block - 1) / block);
     const dim3 grid(static_cast<unsigned>(blocks) * a.splits, a.c.n_heads, a.c.n_seqs);
-    return a.head_dim == 128 ? launch_kernel(paged_attn_f32_rows_kernel<128>, grid, dim3(128), 0, L.stream, a, blocks)
-                             : launch_kernel(paged_attn_f32_rows_kernel<64>, grid, dim3(128), 0, L.stream, a, blocks);
+    return a.head_dim == 128 ? launch_kernel(paged_attn_f32_rows_kernel<128>, grid, dim3(128), kF32RowSmem, L.stream, a, blocks)
+                             : launch_kernel(paged_attn_f32_rows_kernel<64>, grid, dim3(128), kF32RowSmem, L.stream, a, blocks);
   }
   if (a.head_dim == 128) return block == 32 ? launch_f32<128, 2>(L, a) : launch_f32<128, 4>(L, a);
   return block == 32 ? launch_f32<64, 2>(L, a) : launch_f32<64, 4>(L, a);

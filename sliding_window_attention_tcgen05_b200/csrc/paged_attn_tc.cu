@@ -16,15 +16,22 @@ namespace {
 // lie in one page, and one producer warp for K and one for V fetch each run by
 // TMA; rows of a run that holds others than the block's keys, and all rows of
 // odd page sizes, are copied with cp.async into the same 128-byte-swizzled
-// layout (zeros for the others).  K and V tiles alternate in one ring.  One
-// thread per warpgroup issues O += P V as P arrives (written over S as bf16, 64
-// keys at a time), then the next S = Q K^T; the two threads take turns at the
-// second half of P V and S, which keeps the warpgroups out of step, so that
-// one's exponentials run under the other's products (left alone they fell into
-// step: 968 us for the 4 ragged prompts of 4096 tokens over 8192; with one
-// thread for both, whose own issue rate then counts, 937 us).
-// O is rescaled in place only when a row's maximum
-// grows by more than 2^8.
+// layout (zeros for the others).  K and V tiles alternate in one ring.
+// A warp per warpgroup issues O += P V as P arrives (written over S as bf16, 64
+// keys at a time), then the next S = Q K^T.  O is rescaled in place only when
+// a row's maximum grows by more than 2^8.
+//
+// What bounds it: a warpgroup's chain of softmax (about 1700 cycles a tile,
+// 1024 of them MUFU issue), products (12 x 64 behind the last weights) and
+// hand-overs; TMEM (two S, two O of 128 columns) has no room for a second S.
+// So what counts is that one warpgroup's chain runs under the other's: the
+// warps that share a scheduler take turns at their exponentials (left alone the
+// warpgroups fall into step).  Measured for 4 ragged prompts of up to 4096
+// tokens over 8192, 32/8 heads of 128 (819 GFLOP): 780 us (1050 TFLOP/s, 64% of
+// cuBLAS's burst rate); without the turns 837; all weights handed over at once
+// 828, in three parts 830; a quarter of the exponentials on the FMA pipe
+// (range reduction and a polynomial) 895; rows all by cp.async, which feeds an
+// SM 16 bytes a clock, 1026; TMA gathers of four rows 1276.
 constexpr int kTcThreads = 384;   // 2 x 4 softmax warps, 2 issuers, 2 producer warps
 constexpr int kTcKeys = 128;
 constexpr float kTcSlack = 8.0f;
@@ -74,6 +81,14 @@ __device__ __forceinline__ int tc_rows(const TcItem& it, int u) {
   return (min(kTcKeys, it.x1 - it.x0 - u * kTcKeys) + 15) & ~15;
 }
 
+template <class T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -91,6 +106,13 @@ __device__ __forceinline__ void tc_output(uint32_t addr, bool any, uint32_t (&o)
 #pragma unroll
     for (int e = 0; e < 32; ++e) o[e] = 0u;
   }
+}
+
+// mbar_wait, with a first sleep before it starts its clock: nearly every wait
+// ends in that sleep, and reading the global timer takes longer than most.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int where) {
+  if (mbar_try_wait(bar, parity) || mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+  return mbar_wait(bar, parity, w, where);
 }
 
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {   // does not wait
@@ -120,6 +142,11 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ float ex2_ordered(float x) {   // keeps its place among the other asm statements
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -137,7 +164,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   uint8_t* sQ = smem;                    // 2 tiles; a tile = D / 64 halves of [128 rows][128 bytes]
   uint8_t* sKV = smem + 2 * TILE;        // ring: K(0), V(0), K(1), V(1), ...
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + NST * TILE);
-  constexpr int FULL = 0, EMPTY = NST, SF = 2 * NST, PF = SF + 2, PVD = PF + 4, DR = PVD + 2, TK = DR + 2, QF = TK + 2, NBAR = QF + 1;
+  // TK: the turns of warp w of each warpgroup at their scheduler's MUFU.
+  constexpr int FULL = 0, EMPTY = NST, SF = 2 * NST, PF = SF + 2, PVD = PF + 4, DR = PVD + 2, TK = DR + 2, QF = TK + 8, NBAR = QF + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_addr(bars + i); };
@@ -194,7 +222,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       mbar_init(bar(PF + 2 * X + 1), 128);   // and 64 .. 127
       mbar_init(bar(PVD + X), 1);
       mbar_init(bar(DR + X), 1);
-      mbar_init(bar(TK + X), 1);
+      for (int w = 0; w < 4; ++w) mbar_init(bar(TK + 4 * X + w), 1);
     }
     mbar_init(bar(QF), 128 * it.n_act);
     *abort_flag = 0;
@@ -241,7 +269,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         // No free buffer: nothing to issue, so pass on what lands meanwhile.
         if (!tma)
           while (told < u && !__all_sync(0xffffffffu, mbar_test_wait(bar(EMPTY + st), empty))) landed(u - told - 1);
-        const bool w_ok = mbar_wait(bar(EMPTY + st), empty, wc, 70);
+        const bool w_ok = tc_wait(bar(EMPTY + st), empty, wc, 70);
         if (!__all_sync(0xffffffffu, w_ok)) break;
         if (tma) {
           const uint32_t have = __ballot_sync(0xffffffffu, min(min(row[0], row[1]), min(row[2], row[3])) >= 0);
@@ -301,28 +329,41 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         dw.abort_flag = &zero;
         for (int v = max(0, u - NST / 2 - 1); v < u; ++v) {
           const int b = 2 * v + (is_v ? 1 : 0);
-          mbar_wait(bar(FULL + b % NST), (b / NST) & 1, dw, 80);
+          tc_wait(bar(FULL + b % NST), (b / NST) & 1, dw, 80);
         }
       }
-    } else if (lane == 0 && warp - 8 < it.n_act) {
-      // ------------- tensor-core products of warpgroup X
-      const int X = warp - 8;
-      const uint32_t tS = tmem + X * 128, tO = tmem + 256 + X * D;
+    } else if (warp - 8 < it.n_act) {
+      // ------------- tensor-core products of warpgroup X: the whole warp walks the loop, so that the compiler knows its
+      // values to be the same in all lanes and keeps them where the products want them (a product is then issued in 32
+      // cycles, in 85 by a lone thread); one lane issues
+      const int X = uniform(warp - 8), nt = uniform(it.nt);
+      const uint32_t tm = uniform(tmem), tS = tm + X * 128, tO = tm + 256 + X * D;
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTcKeys, 0);
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, 1);
-      const TcTiles tiles = tc_tiles(a, it, X);
+      TcTiles tiles = tc_tiles(a, it, X);
+      tiles.first = uniform(tiles.first);
+      tiles.end = uniform(tiles.end);
+      const int rows_left = uniform(it.x1 - it.x0);
       // Descriptors of the first tiles; a stage or a K step further is an addition to the address field (built anew
       // for each product they take longer than the product).
-      const uint64_t desc_q = smem_desc_sw128(smem_addr(sQ + X * TILE), 16, 1024);
-      const uint64_t desc_k = smem_desc_sw128(smem_addr(sKV), 16, 1024);
-      const uint64_t desc_v = smem_desc_sw128(smem_addr(sKV), kTcKeys * 128, 1024);
-      const bool both = it.n_act == 2;
-      bool ok = it.nt == 0 || mbar_wait(bar(QF), 0, wc, 79);
-      for (int u = -1; ok && u < it.nt; ++u) {   // O += P V of tile u, then S of tile u + 1
-        const int bk = 2 * u + 2, bv = 2 * u + 1, sk = bk % NST, sv = bv % NST, t = u - tiles.first;
+      const uint32_t at_q = uniform(smem_addr(sQ + X * TILE)), at_kv = uniform(smem_addr(sKV));
+      const uint64_t desc_q = smem_desc_sw128(at_q, 16, 1024);
+      const uint64_t desc_k = smem_desc_sw128(at_kv, 16, 1024);
+      const uint64_t desc_v = smem_desc_sw128(at_kv, kTcKeys * 128, 1024);
+      const uint32_t b0 = uniform(bar(0));
+      auto ubar = [&](int i) { return b0 + 8 * i; };
+      const bool lead = elect_one();
+      auto wait = [&](int i, uint32_t parity, int where) {
+        return __all_sync(0xffffffffu, tc_wait(ubar(i), parity, wc, where)) != 0;
+      };
+      bool ok = nt == 0 || wait(QF, 0, 79);
+      int sk = 0, sv = NST - 1;             // stages of K(u + 1) and V(u)
+      uint32_t pk = 0, pvp = 1;             // and their parities
+      for (int u = -1; ok && u < nt; ++u) {   // O += P V of tile u, then S of tile u + 1
+        const int t = u - tiles.first;
         const bool pv = u >= tiles.first && u < tiles.end, sc = u + 1 >= tiles.first && u + 1 < tiles.end;
         const uint64_t dv = desc_v + static_cast<uint32_t>(sv * (TILE >> 4));
-        const int used = tc_rows(it, u);
+        const int used = (min(kTcKeys, rows_left - u * kTcKeys) + 15) & ~15;
         auto half_pv = [&](int half) {
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {   // 16 keys: 8 TMEM columns of P, 16 rows of V
@@ -330,48 +371,56 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
             if (kk * 16 < used) umma_bf16_ts(tO, tS + 8 * kk, dv + kk * (2048 >> 4), idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
           }
         };
-        if (u >= 0 && !(ok = mbar_wait(bar(FULL + sv), (bv / NST) & 1, wc, 73))) break;
+        if (u >= 0 && !(ok = wait(FULL + sv, pvp, 73))) break;
         if (pv) {
-          if (!(ok = mbar_wait(bar(PF + 2 * X), t & 1, wc, 74))) break;
+          if (!(ok = wait(PF + 2 * X, t & 1, 74))) break;
           tc_fence_after();
-          half_pv(0);
+          if (lead) half_pv(0);
         } else if (u >= 0) {
-          mbar_arrive(bar(EMPTY + sv));
+          if (lead) mbar_arrive(ubar(EMPTY + sv));
         }
-        if (u + 1 < it.nt && !(ok = mbar_wait(bar(FULL + sk), (bk / NST) & 1, wc, 71))) break;
-        if (pv && !(ok = mbar_wait(bar(PF + 2 * X + 1), t & 1, wc, 74))) break;
-        if (both && !(ok = mbar_wait(bar(TK + X), (u & 1) ^ X, wc, 72))) break;
+        if (u + 1 < nt && !(ok = wait(FULL + sk, pk, 71))) break;
+        if (pv && !(ok = wait(PF + 2 * X + 1, t & 1, 74))) break;
         tc_fence_after();
-        if (pv) half_pv(1);
-        if (sc) {   // S(u + 1) overwrites P(u), which the product before it has read
-          const uint64_t dk = desc_k + static_cast<uint32_t>(sk * (TILE >> 4));
-          if (pv) {
-            umma_commit(bar(PVD + X));
-            umma_commit(bar(EMPTY + sv));
-          }
+        if (lead) {
+          if (pv) half_pv(1);
+          if (sc) {   // S(u + 1) overwrites P(u), which the product before it has read
+            const uint64_t dk = desc_k + static_cast<uint32_t>(sk * (TILE >> 4));
+            if (pv) {
+              umma_commit(ubar(PVD + X));
+              umma_commit(ubar(EMPTY + sv));
+            }
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = ((kk >> 2) * (kTcKeys * 128) + (kk & 3) * 32) >> 4;
-            umma_bf16(tS, desc_q + o, dk + o, idesc_s, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = ((kk >> 2) * (kTcKeys * 128) + (kk & 3) * 32) >> 4;
+              umma_bf16(tS, desc_q + o, dk + o, idesc_s, kk > 0);
+            }
+            umma_commit(ubar(SF + X));
+          }
+          if (sc) {
+            umma_commit(ubar(EMPTY + sk));
+          } else {
+            if (pv) {
+              umma_commit(ubar(PVD + X));
+              umma_commit(ubar(EMPTY + sv));
+            }
+            if (u + 1 < nt) mbar_arrive(ubar(EMPTY + sk));
           }
         }
-        if (both) mbar_arrive(bar(TK + (X ^ 1)));
-        if (sc) {
-          umma_commit(bar(SF + X));
-          umma_commit(bar(EMPTY + sk));
-        } else {
-          if (pv) {
-            umma_commit(bar(PVD + X));
-            umma_commit(bar(EMPTY + sv));
-          }
-          if (u + 1 < it.nt) mbar_arrive(bar(EMPTY + sk));
-        }
+        __syncwarp();
+        sv = sk + 1 == NST ? 0 : sk + 1;
+        pvp = sk + 1 == NST ? pk ^ 1 : pk;
+        sk = sv + 1 == NST ? 0 : sv + 1;
+        pk = sv + 1 == NST ? pvp ^ 1 : pvp;
       }
-      umma_commit(bar(DR + X));
-      int zero = 0;
-      WaitCtx dw = wc;
-      dw.abort_flag = &zero;
-      mbar_wait(bar(DR + X), 0, dw, 75);
+      if (lead) {
+        umma_commit(ubar(DR + X));
+        int zero = 0;
+        WaitCtx dw = wc;
+        dw.abort_flag = &zero;
+        tc_wait(ubar(DR + X), 0, dw, 75);
+      }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
@@ -408,12 +457,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       const int pre = min(it.kl.pre, it.x1);
       const int all_lo = __reduce_max_sync(0xffffffffu, xlo), all_hi = __reduce_min_sync(0xffffffffu, xhi);
       const TcTiles tiles = tc_tiles(a, it, X);
+      const TcTiles other = tc_tiles(a, it, X ^ 1);
+      const int turns = it.n_act == 2 ? min(tiles.end - tiles.first, other.end - other.first) : 0;
+      const uint32_t turn_mine = bar(TK + 4 * X + (warp & 3)), turn_other = bar(TK + 4 * (X ^ 1) + (warp & 3));
       float m_used = -INFINITY, l_run = 0.f;
       int t = 0;
       bool ok = true;
       for (int u = tiles.first; u < tiles.end; ++u) {
         const int xt = it.x0 + u * kTcKeys;
-        bool w = mbar_wait(bar(SF + X), t & 1, wc, 76);
+        bool w = tc_wait(bar(SF + X), t & 1, wc, 76);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         tc_fence_after();
         float sv[128];
@@ -476,7 +528,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         }
         l_run *= corr;
         if (t > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-          w = mbar_wait(bar(PVD + X), (t - 1) & 1, wc, 77);
+          w = tc_wait(bar(PVD + X), (t - 1) & 1, wc, 77);
           if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
@@ -492,30 +544,57 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         const float mu = m_used == -INFINITY ? 0.f : m_used;
         const uint64_t sc2 = f2_pack(sc, sc), mu2 = f2_pack(-mu, -mu);
         uint64_t rs[2] = {0, 0};   // two packed sums
+        auto args = [&](int c) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
+          for (int e = c * 32; e < c * 32 + 32; e += 2)
+            f2_unpack(ffma2(f2_pack(sv[e], sv[e + 1]), sc2, mu2), sv[e], sv[e + 1]);
+        };
+        args(0);
+        if (t < turns) {
+          w = tc_wait(turn_mine, (t & 1) ^ (X ^ 1), wc, 82);
+          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        }
+        // Quarters of 32 keys: one quarter's sums and packing fill the gaps between the next one's exponentials (the
+        // ordered asm keeps each store behind them).
+        auto exps = [&](int c) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float p0, p1;
-            f2_unpack(ffma2(f2_pack(sv[c * 64 + 2 * e], sv[c * 64 + 2 * e + 1]), sc2, mu2), p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            rs[e & 1] = fadd2(rs[e & 1], f2_pack(p0, p1));
-            pk[e] = pack_bf16x2(p0, p1);
+          for (int e = 0; e < 32; ++e) sv[c * 32 + e] = ex2_ordered(sv[c * 32 + e]);
+        };
+        auto pack = [&](int c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            rs[e & 1] = fadd2(rs[e & 1], f2_pack(sv[c * 32 + 2 * e], sv[c * 32 + 2 * e + 1]));
+            p[e] = pack_bf16x2(sv[c * 32 + 2 * e], sv[c * 32 + 2 * e + 1]);
           }
-          tmem_st32(tS + 32 * c, pk);
+          tmem_st16(tS + 16 * c, p);
+        };
+        auto hand_over = [&](int half) {
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(bar(PF + 2 * X + c));
+          mbar_arrive(bar(PF + 2 * X + half));
+        };
+        args(1); exps(0);
+        args(2); exps(1); args(3);
+        pack(0);
+        exps(2);
+        pack(1);
+        hand_over(0);
+        exps(3);
+        if (t < turns) {   // all exponentials are issued: the other warp's turn
+          __syncwarp();
+          if (lane == 0) mbar_arrive(turn_other);
         }
+        pack(2);
+        pack(3);
+        hand_over(1);
         float r0, r1;
         f2_unpack(fadd2(rs[0], rs[1]), r0, r1);
         l_run += r0 + r1;
         ++t;
       }
       if (ok && t > 0) {
-        const bool w = mbar_wait(bar(PVD + X), (t - 1) & 1, wc, 78);
+        const bool w = tc_wait(bar(PVD + X), (t - 1) & 1, wc, 78);
         ok = __all_sync(0xffffffffu, w);
         tc_fence_after();
       }

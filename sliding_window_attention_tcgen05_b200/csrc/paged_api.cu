@@ -37,13 +37,27 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
   } else {
     p.kernel = 1;
     ctas = lanes * ((rows + 255) / 256);
-    want = ctas >= kPlanSms ? 1 : 2 * kPlanSms;
-    min_keys = 512;
+    want = 1;
+    min_keys = 128;
   }
   int64_t sp = (want + ctas - 1) / ctas;
   const int64_t most = max_kv / min_keys;
   if (sp > most) sp = most;
   if (sp > kMaxSplits) sp = kMaxSplits;
+  if (p.kernel == 1) {
+    // One CTA an SM: the split whose waves take least, in units of a tile of 128 keys (2 us), of which a CTA's start and
+    // end cost about 4 and the joining of parts 3 (4 chunks of 100 tokens over 3000, 8 heads: 33 us in 128 CTAs, 36 us
+    // in 160, which do not run at once).
+    const int64_t tiles = (max_kv + 127) / 128;
+    int64_t best = 0;
+    for (int64_t c = 1; c <= kMaxSplits && c <= (most > 1 ? most : 1); ++c) {
+      const int64_t cost = (ctas * c + kPlanSms - 1) / kPlanSms * ((tiles + c - 1) / c + 4) + (c > 1 ? 3 : 0);
+      if (best == 0 || cost < best) {
+        best = cost;
+        sp = c;
+      }
+    }
+  }
   // Where the rows kernel's CTAs can all run at once (three an SM) with few enough keys each, clusters of up to 8 join
   // their results themselves, which saves the combining launch; with more CTAs than that a cluster holds its places on
   // the SMs until its slowest CTA is done (64 sequences of up to 4096 tokens, 8 K/V heads: 96 us in clusters of 4, 92 us

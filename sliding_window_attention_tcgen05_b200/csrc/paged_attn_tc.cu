@@ -12,7 +12,7 @@ namespace {
 // 128 X .. 128 X + 127 of the block (TMEM lane = row).  Keys are walked in
 // tiles of 128 of the block's key list.  Pages may have any size and the list
 // may start anywhere in one, so a tile's rows lie anywhere: where the page size
-// is a multiple of 16 the list is cut into aligned runs of up to 128 rows that
+// is a multiple of 8 the list is cut into aligned runs of up to 128 rows that
 // lie in one page, and one producer warp for K and one for V fetch each run by
 // TMA; rows of a run that holds others than the block's keys, and all rows of
 // odd page sizes, are copied with cp.async into the same 128-byte-swizzled
@@ -197,7 +197,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
   // Pool rows of four rows of tile u, or -1: lane * 4 + k where runs are fetched
   // by TMA (so that a run's rows are R / 4 neighbouring lanes'), else lane + 32 k.
-  const bool tma = run >= 16;
+  const bool tma = run >= 8;
   auto lookup = [&](int u, int (&row)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -671,11 +671,12 @@ cudaError_t launch_tc(const Launch& L, const PagedAttnArgs& a, int blocks) {
   const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) * a.c.n_heads * a.c.page.d;
   CUtensorMap tk, tv;
   const uint64_t dims[2] = {D, rows}, strides[1] = {D * 2};
-  // Runs: the largest power of two that divides the page size, up to a tile.  Below 16 rows a TMA copy each costs more
-  // than copying the rows with cp.async.
+  // Runs: the largest power of two that divides the page size, up to a tile.  Below 8 rows a TMA copy each costs more
+  // than copying the rows with cp.async (2 chunks of 1000 tokens over 4000, 32/8 heads of 128: pages of 16 to 128 rows
+  // 135 to 137 us, of 8 rows 154, of 8 rows by cp.async 184, of 50 rows by cp.async 172).
   int run = 1;
   while (run < kTcKeys && a.c.page.d % (2 * run) == 0) run *= 2;
-  if (run < 16) run = 1;
+  if (run < 8) run = 1;
   const uint32_t box[2] = {64, static_cast<uint32_t>(run)};
   if (!encode_tmap(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tmap(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))

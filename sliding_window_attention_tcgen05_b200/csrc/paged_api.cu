@@ -449,7 +449,7 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
            : plan.kernel == 1 ? launch_paged_attn_tc(L, a)
                               : launch_paged_attn_f32(L, a);
   }));
-  if (a.parts > 1)
+  if (a.parts > 1 && a.scores == nullptr)   // with kept scores the sum of the weights does it
     VX_CUDA(traced(L, "paged_attn_combine", 1, [&] { return launch_paged_attn_combine(L, a, bf16); }));
   if (track)
     VX_CUDA(traced(L, "paged_attn_weights", plan.w_segs > 1 && !plan.keep_scores ? 2 : 1, [&] { return launch_paged_attn_weights(L, a, bf16, kv); }));

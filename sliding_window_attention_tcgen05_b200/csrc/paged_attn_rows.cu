@@ -778,49 +778,52 @@ __global__ void __launch_bounds__(128) paged_attn_f32_rows_kernel(const __grid_c
 constexpr int kCombineThreads = 256;
 constexpr int kCombineDeep = 8;   // loads in flight
 
-template <int D, bool BF16, int W>
-__global__ void __launch_bounds__(kCombineThreads) paged_attn_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int V = D / 32, RB = kCombineThreads / 32 / W;   // rows of a block
-  __shared__ float part[RB][W][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp / W, w = warp % W;
+// The parts' largest maximum M, their factors 2^(m - M) and the sum l of a row,
+// by one warp.
+struct PartSums {
+  float M, l, wt[kMaxSplits / 32];   // wt[i]: of part i * 32 + lane
+};
+__device__ __forceinline__ PartSums part_sums(const PagedAttnArgs& a, int64_t row) {
   const int64_t rows = static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * RB + rb;
+  const int lane = threadIdx.x & 31;
+  PartSums r;
+  r.M = -INFINITY;
+  r.l = 0.f;
+  float2 ml[kMaxSplits / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 32; ++i) {
+    const int sp = i * 32 + lane;
+    ml[i] = sp < a.parts ? a.part_ml[sp * rows + row] : make_float2(-INFINITY, 0.f);
+    r.M = fmaxf(r.M, ml[i].x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) r.M = fmaxf(r.M, __shfl_xor_sync(0xffffffffu, r.M, off));
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 32; ++i) {
+    r.wt[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - r.M);
+    r.l += ml[i].y * r.wt[i];
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) r.l += __shfl_xor_sync(0xffffffffu, r.l, off);
+  return r;
+}
+
+// The row of this thread's W warps; part: shared memory of all 8 warps.  Every thread of the block calls it.
+template <int D, bool BF16, int W>
+__device__ __forceinline__ void combine_row(const PagedAttnArgs& a, int64_t row, bool mine, float (*part)[D]) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
+  const int64_t rows = static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
   const int64_t tok = row / a.n_q_heads;
   const int h = static_cast<int>(row - tok * a.n_q_heads);
-  bool mine = row < rows;
-  if (mine) {
-    // Rows outside every sequence (or past max_q) have no parts: find the row's sequence.
-    int lo = 0, hi = a.c.n_seqs;   // last s with q_start[s] <= tok
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.ch.q_start[mid] <= tok) lo = mid; else hi = mid;
-    }
-    const SeqSpan q = seq_span(a.c, a.ch, lo);
-    mine = tok >= q.row0 && tok < q.row0 + q.n;
-  }
   float M = -INFINITY, l = 0.f, y[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) y[e] = 0.f;
   if (mine) {
-    float2 ml[kMaxSplits / 32];
-#pragma unroll
-    for (int i = 0; i < kMaxSplits / 32; ++i) {
-      const int sp = i * 32 + lane;
-      ml[i] = sp < a.parts ? a.part_ml[sp * rows + row] : make_float2(-INFINITY, 0.f);
-      M = fmaxf(M, ml[i].x);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float wt[kMaxSplits / 32];
-#pragma unroll
-    for (int i = 0; i < kMaxSplits / 32; ++i) {
-      wt[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - M);
-      l += ml[i].y * wt[i];
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    const PartSums ps = part_sums(a, row);
+    M = ps.M;
+    l = ps.l;
+    const float(&wt)[kMaxSplits / 32] = ps.wt;
 #pragma unroll
     for (int i = 0; i < kMaxSplits / 32; ++i)
       for (int j0 = w; j0 < 32 && i * 32 + j0 < a.parts; j0 += W * kCombineDeep) {
@@ -842,13 +845,13 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine_kernel(con
   }
   if constexpr (W > 1) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) part[rb][w][lane * V + e] = y[e];
+    for (int e = 0; e < V; ++e) part[warp][lane * V + e] = y[e];
     __syncthreads();
     if (w > 0) return;
 #pragma unroll
     for (int k = 1; k < W; ++k)
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] += part[rb][k][lane * V + e];
+      for (int e = 0; e < V; ++e) y[e] += part[warp + k][lane * V + e];
   }
   if (!mine) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -862,6 +865,28 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine_kernel(con
     for (int e = 0; e < V; ++e) dst[e] = y[e] * inv;
   }
   if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
+template <int D, bool BF16, int W>
+__global__ void __launch_bounds__(kCombineThreads) paged_attn_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int WARPS = kCombineThreads / 32;
+  __shared__ float part[WARPS][D];
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (WARPS / W) + (threadIdx.x >> 5) / W;
+  const int64_t tok = row / a.n_q_heads;
+  bool mine = row < static_cast<int64_t>(a.ch.n_tokens) * a.n_q_heads;
+  if (mine) {
+    // Rows outside every sequence (or past max_q) have no parts: find the row's sequence.
+    int lo = 0, hi = a.c.n_seqs;   // last s with q_start[s] <= tok
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.ch.q_start[mid] <= tok) lo = mid; else hi = mid;
+    }
+    const SeqSpan q = seq_span(a.c, a.ch, lo);
+    mine = tok >= q.row0 && tok < q.row0 + q.n;
+  }
+  combine_row<D, BF16, W>(a, row, mine, part);
 }
 
 // ---------------------------------------------------------------- weights --
@@ -1036,27 +1061,47 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
   }
 }
 
-// The same sum from the scores that the rows kernel kept (base 2, by list
+// The same sum from the scores that the rows kernels kept (base 2, by list
 // position; up to 8 rows, so that writing and reading them costs less than
-// reading K again).  A thread per slot.
+// reading K again).  A thread per slot.  Where the keys were split, the grid has
+// a block more for each row, which joins the row's parts, and the others take
+// the rows' log-sum-exps from the parts themselves: one launch for both.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a) {
+__global__ void __launch_bounds__(kCombineThreads)
+paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a, int blocks) {
   pdl_wait();
   pdl_trigger();
   __shared__ float s_lse[8];
+  __shared__ float part[kCombineThreads / 32][D];
   const int kh = blockIdx.y, s = blockIdx.z;
   const SeqSpan q = seq_span(a.c, a.ch, s);
   if (q.n <= 0) return;
   const int G = a.group, rows = q.n * G, cap = a.ch.max_q * G;
-  if (threadIdx.x < rows) {
-    const int t = a.group_div.div(threadIdx.x), h = kh * G + threadIdx.x - t * G;
-    const float z = a.lse[static_cast<int64_t>(q.row0 + t) * a.n_q_heads + h];
-    s_lse[threadIdx.x] = z == -INFINITY ? INFINITY : z * kLog2e;   // weight 0 without a sum
+  auto row_of = [&](int r) -> int64_t {
+    const int t = a.group_div.div(r);
+    return static_cast<int64_t>(q.row0 + t) * a.n_q_heads + kh * G + r - t * G;
+  };
+  if (static_cast<int>(blockIdx.x) >= blocks) {
+    const int r = static_cast<int>(blockIdx.x) - blocks;
+    if (r < rows) combine_row<D, BF16, kCombineThreads / 32>(a, row_of(r), true, part);
+    return;
+  }
+  const int warp = threadIdx.x >> 5;
+  if (warp < rows) {   // base 2; +inf (weight 0) without a sum
+    float z;
+    if (a.parts > 1) {
+      const PartSums ps = part_sums(a, row_of(warp));
+      z = ps.l == 0.f ? INFINITY : ps.M + log2f(ps.l);
+    } else {
+      z = a.lse[row_of(warp)];
+      z = z == -INFINITY ? INFINITY : z * kLog2e;
+    }
+    s_lse[warp] = z;
   }
   __syncthreads();
   const KeyList kl = key_list(q.old, q.old + q.n - 1, a.window, a.prefix ? a.prefix[s] : 0, q.kv);
   const float* kept = a.scores + (static_cast<int64_t>(s) * a.c.n_heads + kh) * cap * a.score_stride;
-  for (int j = blockIdx.x * 256 + threadIdx.x; j < q.kv; j += gridDim.x * 256) {
+  for (int j = blockIdx.x * kCombineThreads + threadIdx.x; j < q.kv; j += blocks * kCombineThreads) {
     const int x = j < kl.cut ? j : j - kl.shift;
     const int row = slot_row(a.c, s, kh, j);
     float sum = 0.f;
@@ -1293,12 +1338,14 @@ cudaError_t launch_paged_attn_combine(const Launch& L, const PagedAttnArgs& a, b
 cudaError_t launch_paged_attn_weights(const Launch& L, const PagedAttnArgs& a, bool bf16, int64_t max_kv) {
   const bool mod = a.cap > 0.f || a.slopes != nullptr;
   if (a.scores != nullptr) {
-    const dim3 g(static_cast<unsigned>((max_kv + 255) / 256), a.c.n_heads, a.c.n_seqs);
+    const int blocks = static_cast<int>((max_kv + kCombineThreads - 1) / kCombineThreads);
+    const dim3 g(static_cast<unsigned>(blocks + (a.parts > 1 ? a.ch.max_q * a.group : 0)), a.c.n_heads, a.c.n_seqs);
+    const dim3 t(kCombineThreads);
     if (a.head_dim == 128)
-      return bf16 ? launch_kernel(paged_attn_weights_kept_kernel<128, true>, g, dim3(256), 0, L.stream, a)
-                  : launch_kernel(paged_attn_weights_kept_kernel<128, false>, g, dim3(256), 0, L.stream, a);
-    return bf16 ? launch_kernel(paged_attn_weights_kept_kernel<64, true>, g, dim3(256), 0, L.stream, a)
-                : launch_kernel(paged_attn_weights_kept_kernel<64, false>, g, dim3(256), 0, L.stream, a);
+      return bf16 ? launch_kernel(paged_attn_weights_kept_kernel<128, true>, g, t, 0, L.stream, a, blocks)
+                  : launch_kernel(paged_attn_weights_kept_kernel<128, false>, g, t, 0, L.stream, a, blocks);
+    return bf16 ? launch_kernel(paged_attn_weights_kept_kernel<64, true>, g, t, 0, L.stream, a, blocks)
+                : launch_kernel(paged_attn_weights_kept_kernel<64, false>, g, t, 0, L.stream, a, blocks);
   }
   const int keys = bf16 ? kWKeys : kWKeysF32;
   const dim3 grid(static_cast<unsigned>((max_kv + keys - 1) / keys * a.w_segs), a.c.n_heads, a.c.n_seqs);

@@ -66,9 +66,10 @@ __device__ __forceinline__ void st1(void* p, int64_t e, float x) {
 // 2 pairs / V units of one vector; then (D - 2 pairs) / V copies.
 //
 // A thread takes one unit at a time: what counts is the number of threads in
-// flight (16384 rows of 40 heads of 128, bf16: 63 us; two units a thread at 48
-// registers 66, four at 78 registers 77).
+// flight (16384 rows of 40 heads of 128, bf16: 57 us, 89% of copy bandwidth; two
+// units a thread at 48 registers 66, four at 78 registers 77).
 constexpr int kRopeBlocks = 6;   // resident blocks an SM: at most 40 registers
+constexpr int kAppendBlocks = 5;   // 48 (prompts of up to 4001 tokens, 32 + 8 + 8 heads of 128: 68 us; at 64 registers 72)
 
 // Place of pair m among a token's cosines and sines: a unit of G pairs reads
 // them two by two, and the same two of neighbouring units are neighbours, so
@@ -81,33 +82,42 @@ __device__ __forceinline__ int cs_place(int m, int pairs) {
 
 struct Unit {
   const uint8_t* src;
-  uint8_t* dst;
-  const float4* cs;     // of the unit's first two pairs; null: a copy
+  int first;            // its first two pairs among the token's float4s; below 0: a copy
+  int at;               // bytes from the head's start, source and destination
 };
 
-// Unit u of a head whose elements start at src / dst; cs: the token's cosines and sines.
+// Unit u of a head whose elements start at src.
 template <bool BF16, bool INTER>
-__device__ __forceinline__ Unit rope_unit(const uint8_t* src, uint8_t* dst, int u, int pairs, const float2* cs) {
+__device__ __forceinline__ Unit rope_unit(const uint8_t* src, int u, int pairs) {
   const int nrot = (INTER ? 2 * pairs : pairs) / Vec<BF16>::N;
   const bool rot = u < nrot;
   const int o = (rot || INTER ? u : u + nrot) * 16;
-  return {src + o, dst + o, rot ? reinterpret_cast<const float4*>(cs) + u : nullptr};
+  return {src + o, rot ? u : -1, o};
 }
 
 template <bool BF16, bool INTER>
-__device__ __forceinline__ void run_unit(const Unit& w, int pairs) {
+__device__ __forceinline__ void load_unit(const Unit& w, int pairs, uint4& x, uint4& x1) {
+  x = *reinterpret_cast<const uint4*>(w.src);
+  if (!INTER && w.first >= 0) x1 = *reinterpret_cast<const uint4*>(w.src + pairs * (BF16 ? 2 : 4));
+}
+
+// dst: where the head's elements go; cs: the token's cosines and sines.
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void store_unit(const Unit& w, int pairs, const uint4& x, const uint4& x1, uint8_t* dst,
+                                           const float2* cs) {
   constexpr int V = Vec<BF16>::N;
-  const uint4 x = *reinterpret_cast<const uint4*>(w.src);
-  if (w.cs == nullptr) {
-    *reinterpret_cast<uint4*>(w.dst) = x;
+  dst += w.at;
+  if (w.first < 0) {
+    *reinterpret_cast<uint4*>(dst) = x;
     return;
   }
+  const float4* c4 = reinterpret_cast<const float4*>(cs) + w.first;
   const int nu = pairs / (INTER ? V / 2 : V);
   Vec<BF16> a(x);
   if constexpr (INTER) {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-      const float4 c = w.cs[i / 4 * nu];
+      const float4 c = c4[i / 4 * nu];
       const float y = a.f[i] * c.x - a.f[i + 1] * c.y, z = a.f[i + 2] * c.z - a.f[i + 3] * c.w;
       a.f[i + 1] = a.f[i + 1] * c.x + a.f[i] * c.y;
       a.f[i + 3] = a.f[i + 3] * c.z + a.f[i + 2] * c.w;
@@ -116,19 +126,19 @@ __device__ __forceinline__ void run_unit(const Unit& w, int pairs) {
     }
   } else {
     const int half = pairs * (BF16 ? 2 : 4);   // bytes from m to m + pairs
-    Vec<BF16> b(*reinterpret_cast<const uint4*>(w.src + half));
+    Vec<BF16> b(x1);
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
-      const float4 c = w.cs[i / 2 * nu];
+      const float4 c = c4[i / 2 * nu];
       const float y = a.f[i] * c.x - b.f[i] * c.y, z = a.f[i + 1] * c.z - b.f[i + 1] * c.w;
       b.f[i] = b.f[i] * c.x + a.f[i] * c.y;
       b.f[i + 1] = b.f[i + 1] * c.z + a.f[i + 1] * c.w;
       a.f[i] = y;
       a.f[i + 1] = z;
     }
-    *reinterpret_cast<uint4*>(w.dst + half) = b.bits();
+    *reinterpret_cast<uint4*>(dst + half) = b.bits();
   }
-  *reinterpret_cast<uint4*>(w.dst) = a.bits();
+  *reinterpret_cast<uint4*>(dst) = a.bits();
 }
 
 // Block: `tok` tokens of the chunk (their cosines and sines computed once in
@@ -153,10 +163,12 @@ __global__ void __launch_bounds__(256, kRopeBlocks) rope_fwd_kernel(const __grid
       const int rh = a.units.div(i), u = i - rh * static_cast<int>(a.units.d);
       const int r = a.heads.div(rh), h = rh - r * a.n_heads;
       const Unit w = rope_unit<BF16, INTER>(
-          static_cast<const uint8_t*>(a.x.p) + ((t0 + r) * a.x.row + h * a.x.head) * ES,
-          static_cast<uint8_t*>(a.y) + ((t0 + r) * a.y_row + h * a.y_head) * ES, u, t.pairs, cs + r * t.pairs);
-      if (w.cs == nullptr && a.in_place) continue;
-      run_unit<BF16, INTER>(w, t.pairs);
+          static_cast<const uint8_t*>(a.x.p) + ((t0 + r) * a.x.row + h * a.x.head) * ES, u, t.pairs);
+      if (w.first < 0 && a.in_place) continue;
+      uint4 x, x1;
+      load_unit<BF16, INTER>(w, t.pairs, x, x1);
+      store_unit<BF16, INTER>(w, t.pairs, x, x1, static_cast<uint8_t*>(a.y) + ((t0 + r) * a.y_row + h * a.y_head) * ES,
+                              cs + r * t.pairs);
     }
   } else {   // element by element: unit = one pair, or one copied element
     for (int i = threadIdx.x; i < items; i += blockDim.x) {
@@ -180,7 +192,7 @@ __global__ void __launch_bounds__(256, kRopeBlocks) rope_fwd_kernel(const __grid
 // unit) with the heads numbered q, k, v; v (and all of them without rope) is
 // copied in 16-byte units.
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(256, kRopeBlocks) paged_append_kernel(const __grid_constant__ AppendArgs a,
+__global__ void __launch_bounds__(256, kAppendBlocks) paged_append_kernel(const __grid_constant__ AppendArgs a,
                                                            const __grid_constant__ RopeTable t, int tok) {
   pdl_wait();
   pdl_trigger();
@@ -192,6 +204,40 @@ __global__ void __launch_bounds__(256, kRopeBlocks) paged_append_kernel(const __
   const int nt = min(sp.n - t0, tok);
   if (nt <= 0) return;
   if (sp.over && threadIdx.x == 0) report_bad_cache(a.status, s);
+  constexpr int ES = BF16 ? 2 : 4;
+  const int row_bytes = a.head_dim * ES, cu = row_bytes / 16, ps = a.c.page.d;
+  const int Hk = a.c.n_heads, Hq = a.n_q_heads, ru = a.units.d;
+  const int64_t g0 = sp.row0 + t0;
+  const int nrot = (Hq + Hk) * ru, items = nt * static_cast<int>(a.per.d);
+  // Item i: its unit, token and head (q, k, v in turn).  A thread's next item is read while it works on one, the first
+  // one under the page look-up and the angles.
+  struct Item {
+    Unit w;
+    int r, h;
+  };
+  auto item = [&](int i) {
+    Item it;
+    it.r = a.per.div(i);
+    const int x = i - it.r * static_cast<int>(a.per.d);
+    if (x < nrot) {
+      it.h = a.units.div(x);
+      const uint8_t* src =
+          it.h < Hq ? static_cast<const uint8_t*>(a.q.p) + ((g0 + it.r) * a.q.row + it.h * a.q.head) * ES
+                    : static_cast<const uint8_t*>(a.k.p) + ((g0 + it.r) * a.k.row + (it.h - Hq) * a.k.head) * ES;
+      it.w = rope_unit<BF16, INTER>(src, x - it.h * ru, t.pairs);
+    } else {
+      const int h = (x - nrot) / cu, o = ((x - nrot) - h * cu) * 16;
+      it.h = Hq + Hk + h;
+      it.w = {static_cast<const uint8_t*>(a.v.p) + ((g0 + it.r) * a.v.row + h * a.v.head) * ES + o, -1, o};
+    }
+    return it;
+  };
+  Item next = {};
+  uint4 n0, n1;
+  if (static_cast<int>(threadIdx.x) < items) {
+    next = item(threadIdx.x);
+    load_unit<BF16, INTER>(next.w, t.pairs, n0, n1);
+  }
   if (t.pairs > 0) {
     const int64_t pos0 = a.pos[s] + t0;
     for (int i = threadIdx.x; i < nt * t.pairs; i += blockDim.x) {
@@ -206,38 +252,25 @@ __global__ void __launch_bounds__(256, kRopeBlocks) paged_append_kernel(const __
     s_row[threadIdx.x] = row;
   }
   __syncthreads();
-  constexpr int ES = BF16 ? 2 : 4;
-  const int row_bytes = a.head_dim * ES, cu = row_bytes / 16, ps = a.c.page.d;
-  const int Hk = a.c.n_heads, Hq = a.n_q_heads, ru = a.units.d;
-  const int64_t g0 = sp.row0 + t0;
-  const int nrot = (Hq + Hk) * ru, items = nt * static_cast<int>(a.per.d);
   for (int i = threadIdx.x; i < items; i += 256) {
-    const int r = a.per.div(i), x = i - r * static_cast<int>(a.per.d);
-    const int64_t to = s_row[r];
-    const float2* c = cs + r * t.pairs;
-    Unit w;
-    if (x < nrot) {
-      const int h = a.units.div(x), u = x - h * ru;
-      if (h < Hq) {
-        w = rope_unit<BF16, INTER>(static_cast<const uint8_t*>(a.q.p) + ((g0 + r) * a.q.row + h * a.q.head) * ES,
-                                   static_cast<uint8_t*>(a.q_out) + ((g0 + r) * a.qo_row + h * a.qo_head) * ES, u,
-                                   t.pairs, c);
-        if (w.cs == nullptr && w.src == w.dst) continue;   // in place
-      } else {
-        if (to < 0) continue;
-        w = rope_unit<BF16, INTER>(static_cast<const uint8_t*>(a.k.p) + ((g0 + r) * a.k.row + (h - Hq) * a.k.head) * ES,
-                                   static_cast<uint8_t*>(a.k_pool) + (to + static_cast<int64_t>(h - Hq) * ps) * row_bytes,
-                                   u, t.pairs, c);
-      }
-    } else {
-      if (to < 0) continue;
-      const int h = (x - nrot) / cu, u = (x - nrot) - h * cu;
-      const int64_t row = to + static_cast<int64_t>(h) * ps;
-      w = {static_cast<const uint8_t*>(a.v.p) + ((g0 + r) * a.v.row + h * a.v.head) * ES + u * 16,
-           static_cast<uint8_t*>(a.v_pool) + row * row_bytes + u * 16, nullptr};
-      if (a.acc != nullptr && u == 0) a.acc[row] = 0.f;
+    const Item it = next;
+    const uint4 x = n0, x1 = n1;
+    if (i + 256 < items) {
+      next = item(i + 256);
+      load_unit<BF16, INTER>(next.w, t.pairs, n0, n1);
     }
-    run_unit<BF16, INTER>(w, t.pairs);
+    uint8_t* dst;
+    if (it.h < Hq) {
+      dst = static_cast<uint8_t*>(a.q_out) + ((g0 + it.r) * a.qo_row + it.h * a.qo_head) * ES;
+    } else {
+      const int64_t to = s_row[it.r];
+      if (to < 0) continue;
+      const bool is_v = it.h >= Hq + Hk;
+      const int64_t row = to + static_cast<int64_t>(it.h - Hq - (is_v ? Hk : 0)) * ps;
+      dst = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + row * row_bytes;
+      if (is_v && a.acc != nullptr && it.w.at == 0) a.acc[row] = 0.f;
+    }
+    store_unit<BF16, INTER>(it.w, t.pairs, x, x1, dst, cs + it.r * t.pairs);
   }
 }
 
@@ -318,7 +351,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int max_keys) {
   const float* acc = a.acc + l * a.src_layer_rows;
   const int run = (n + C * T - 1) / (C * T) * 32;    // slots of a warp
   const int c0 = min(c * (T / 32) * run, n), c1 = min(c0 + (T / 32) * run, n);
-  const bool fits = (T / 32) * run <= max_keys;
+  const bool fits = c1 - c0 <= max_keys;
   auto from_pool = [&](int j) -> uint32_t {
     const int row = slot_row(a.src, s, h, j);
     return row < 0 ? 0u : weight_key(acc[row]);
@@ -430,7 +463,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int max_keys) {
 // so a CTA that walks all blocks in order, reading a block before it writes it,
 // never overwrites a row it still has to read (slices are independent).
 constexpr int kMoveThreads = 256;
-constexpr int kMoveDeep = 4;
+constexpr int kMoveDeep = 4;   // 2: 64 sequences of 1000 slots to 750 in 204 instead of 160 us, 8: no gain
 constexpr int kMoveChunks = kMoveThreads * kMoveDeep;
 constexpr int kMoveMaxRows = 256;   // of a block: slices of at least 4 chunks
 

@@ -323,7 +323,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       }
       while (!tma && u == it.nt && told < u) landed(u - told - 1);
       cp_async_wait<0>();
-      if (tma && u < it.nt) {   // gave up: the copies in flight must land before the CTA ends
+      if (tma && (u < it.nt || *abort_flag)) {   // gave up: the copies in flight must land before the CTA ends
         int zero = 0;
         WaitCtx dw = wc;
         dw.abort_flag = &zero;

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -62,6 +62,9 @@ class RopeCfg:
 
     def c(self) -> VxRopeCfg:
         return self._c
+
+    def __getstate__(self):   # a copy or another process makes its own C structure
+        return {f.name: getattr(self, f.name) for f in fields(self)}
 
     @functools.cached_property
     def _address(self) -> int:

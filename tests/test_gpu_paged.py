@@ -345,6 +345,10 @@ _ATTN = [   # olds, news, hq, hkv, D, page, options
     ([200, 31], [64, 200], 4, 2, 128, 100, dict(slopes=True, window=70)),
     ([0, 9], [200, 150], 2, 2, 64, 65536, dict(prefix=[500, 40])),       # a prefix behind the sequence's end
     ([300, 8], [90, 33], 4, 2, 64, 16, dict(scale=0.5)),
+    ([300, 0], [300, 129], 2, 2, 64, 16, dict(window=1)),                # the warpgroups' tiles part
+    ([1000, 77], [256, 300], 1, 1, 128, 128, dict(window=129)),
+    ([520, 64], [700, 260], 1, 1, 128, 8, dict(window=40, prefix=[130, 3])),
+    ([40, 3, 0], [2, 1, 3], 5, 1, 128, 16, dict(prefix=[9, 3, 0])),      # 9 to 16 rows
 ]
 
 
@@ -435,6 +439,51 @@ def test_large_scores_and_nan(n, D, dtype):
     b.cache.k[0, pg.cuda(), :, off.cuda()] = float("nan")
     o, lse = vx.paged_attn_fwd(b.cache, 0, b.q.cuda(), b.q_start, n, return_lse=True)
     assert torch.isnan(o).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("dtype,n,D", [(BF, 2, 128), (BF, 150, 128), (BF, 150, 64), (F32, 2, 128), (F32, 70, 128)])
+def test_pools_past_32_bit_offsets(dtype, n, D):
+    # The sequences' pages at the end of a pool whose bytes and elements need more than 32 bits (5 GB of K).
+    vx = _vx()
+    b = Batch([300, 45], [n, n], 4, 2, D, 16, dtype, weights=True, room=2 * n)
+    small = b.cache
+    m = small.k.shape[1]
+    P = (5 << 30) // (2 * 16 * D * small.k.element_size()) + m
+    c = vx.PagedCache(1, P, 16, 2, D, 2, small.table.shape[1], dtype=dtype, weights=True)
+    for name in ("k", "v", "acc"):
+        getattr(c, name)[:, -m:] = getattr(small, name)
+    c.table.copy_(torch.where(small.table >= 0, small.table + (P - m), small.table))
+    c.lens.copy_(small.lens)
+    c.pos.copy_(small.pos)
+    ws = vx.Workspace(1 << 24)
+    vx.status_reset(ws)
+    gen = torch.Generator().manual_seed(5)
+    row = _randn((2 * n, 4 + 2 * 2, D), dtype, gen).cuda()
+    for cache in (small, c):
+        q = vx.paged_append(cache, 0, row[:, 4:6], row[:, 6:], b.q_start, n, rope=vx.RopeCfg(theta=1e4), q=row[:, :4],
+                            ws=ws)
+        cache.out = vx.paged_attn_fwd(cache, 0, q, b.q_start, n, track=0.5, return_lse=True, ws=ws)
+        vx.paged_advance(cache, b.q_start, 2 * n, n, ws=ws)
+        vx.paged_evict(cache, 200, 20, ws=ws)
+    assert vx.status_check(ws) == 0
+    for x, y in zip(small.out, c.out):
+        assert torch.equal(x, y)
+    for name in ("k", "v", "acc"):
+        assert torch.equal(getattr(c, name)[:, -m:].nan_to_num(), getattr(small, name).nan_to_num())
+        assert not getattr(c, name)[:, :-m].any()
+    assert torch.equal(c.lens, small.lens)
+
+
+def test_rotary_configurations_are_copied_and_pickled():
+    import copy
+    import pickle
+    vx = _vx()
+    x, pos = torch.randn(4, 2, 64, device="cuda"), torch.arange(4, device="cuda")
+    cfg = vx.RopeCfg(theta=1e4, rot_dim=32)
+    want = vx.rope_fwd(x, pos, cfg)
+    for other in (copy.deepcopy(cfg), copy.copy(cfg), pickle.loads(pickle.dumps(cfg))):
+        assert other == cfg and other._address != cfg._address
+        assert torch.equal(vx.rope_fwd(x, pos, other), want)
 
 
 @pytest.mark.parametrize("case", ["empty", "none"])

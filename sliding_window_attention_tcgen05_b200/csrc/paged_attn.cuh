@@ -77,13 +77,43 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// Packed fp32 pairs (each half rounds like the scalar operation).
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Scores to the exponent's base-2 units.  Without cap and slopes that is one
-// multiplication by scale * log2(e).  cap * tanh(z) = cap * (1 - 2 / (e^{2z} + 1)),
-// from one exponential and half a reciprocal (absolute error about cap * 2^-22,
-// where the hardware's own tanh would leave cap * 2^-11).
+// multiplication by scale * log2(e).  A cap in bf16: where all of a thread's
+// scores are at most half the cap, as they are nearly always, cap * tanh(z) =
+// score * P(z^2) with the minimax polynomial P of tanh(z) / z on z^2 <= 1/4
+// (relative error 1.3e-8), on the FMA pipe alone; else cap * (1 - 2 / (e^{2z} +
+// 1)), from one exponential and half a reciprocal (absolute error about cap *
+// 2^-22, where the hardware's own tanh would leave cap * 2^-11).  fp32: tanhf,
+// whose error is relative to the score too.
 struct ScoreMod {
   float sl2;       // scale * log2 e
   float cap2;      // cap * log2 e, 0 = no cap
+  float z;         // scale / cap
   float two_z;     // 2 scale / cap * log2 e
   bool bias;       // slopes
 };
@@ -91,7 +121,8 @@ __device__ __forceinline__ ScoreMod score_mod(const PagedAttnArgs& a) {
   ScoreMod m;
   m.sl2 = a.scale * kLog2e;
   m.cap2 = a.cap * kLog2e;
-  m.two_z = a.cap > 0.f ? 2.f * a.scale / a.cap * kLog2e : 0.f;
+  m.z = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  m.two_z = 2.f * m.z * kLog2e;
   m.bias = a.slopes != nullptr;
   return m;
 }
@@ -100,33 +131,44 @@ __device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either 
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
-// N raw scores, two at a time: 1 / a and 1 / b from one reciprocal of a b (exponents up to 2^60, beyond which tanh is 1
-// to the last bit, so that the product stays finite).
+// N raw scores.
 template <int N>
 __device__ __forceinline__ void scale_scores(const ScoreMod& m, float (&s)[N]) {
   if (m.cap2 > 0.f) {
+    float big = 0.f;
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
-      const float a = ex2_approx(min_nan(s[e] * m.two_z, 60.f)) + 1.f;
-      const float b = ex2_approx(min_nan(s[e + 1] * m.two_z, 60.f)) + 1.f;
-      const float r = -2.f * m.cap2 * rcp_approx(a * b);
-      s[e] = fmaf(r, b, m.cap2);
-      s[e + 1] = fmaf(r, a, m.cap2);
+    for (int e = 0; e < N; ++e) big = fmaxf(big, fabsf(s[e]));
+    if (big * fabsf(m.z) <= 0.5f) {
+      const uint64_t z = f2_pack(m.z, m.z), sl = f2_pack(m.sl2, m.sl2);
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        const uint64_t x = f2_pack(s[e], s[e + 1]), u = fmul2(x, z), w = fmul2(u, u);
+        uint64_t p = f2_pack(0.0171350073f, 0.0171350073f);
+        p = ffma2(p, w, f2_pack(-0.0529860742f, -0.0529860742f));
+        p = ffma2(p, w, f2_pack(0.133247793f, 0.133247793f));
+        p = ffma2(p, w, f2_pack(-0.333330691f, -0.333330691f));
+        p = ffma2(p, w, f2_pack(1.f, 1.f));
+        f2_unpack(fmul2(fmul2(x, sl), p), s[e], s[e + 1]);
+      }
+    } else {   // two at a time: 1 / a and 1 / b from one reciprocal of a b (exponents up to 2^60, beyond which tanh is 1
+               // to the last bit, so that the product stays finite)
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        const float a = ex2_approx(min_nan(s[e] * m.two_z, 60.f)) + 1.f;
+        const float b = ex2_approx(min_nan(s[e + 1] * m.two_z, 60.f)) + 1.f;
+        const float r = -2.f * m.cap2 * rcp_approx(a * b);
+        s[e] = fmaf(r, b, m.cap2);
+        s[e + 1] = fmaf(r, a, m.cap2);
+      }
     }
   } else {
 #pragma unroll
     for (int e = 0; e < N; ++e) s[e] *= m.sl2;
   }
 }
-// slope2 = slope of the head * log2 e, dist = i - j
+// A score of the fp32 kernels; slope2 = slope of the head * log2 e, dist = i - j.
 __device__ __forceinline__ float score2(const ScoreMod& m, float s, float slope2, int dist) {
-  float y;
-  if (m.cap2 > 0.f) {
-    const float e = ex2_approx(s * m.two_z);
-    y = m.cap2 - 2.f * m.cap2 * rcp_approx(e + 1.f);
-  } else {
-    y = s * m.sl2;
-  }
+  const float y = m.cap2 > 0.f ? m.cap2 * tanhf(s * m.z) : s * m.sl2;
   return y - slope2 * static_cast<float>(abs(dist));
 }
 

@@ -486,6 +486,17 @@ def test_rotary_configurations_are_copied_and_pickled():
         assert torch.equal(vx.rope_fwd(x, pos, other), want)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,D", [(2, 64), (12, 128), (150, 64), (150, 128)])
+@pytest.mark.parametrize("scale,cap", [(0.5, 50.0), (1.0, 6.0), (8.0, 2.0), (60.0, 10.0)])
+def test_capped_scores_small_and_large(dtype, n, D, scale, cap):
+    # Scores well below the cap, around half of it, and far above it (both sides of the kernels' choice of formula).
+    vx = _vx()
+    b = Batch([140, 9], [n, n], 4, 2, D, 16, dtype, scale=scale, weights=True)
+    o, lse = vx.paged_attn_fwd(b.cache, 0, b.q.cuda(), b.q_start, n, cap=cap, track=0.0, return_lse=True)
+    _check_attn(b, o, lse, cap=cap, track=0.0)
+
+
 @pytest.mark.parametrize("case", ["empty", "none"])
 def test_no_rows(case):
     vx = _vx()

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256, kAppendBlocks) paged_append_kernel(const 
   if (nt <= 0) return;
   if (sp.over && threadIdx.x == 0) report_bad_cache(a.status, s);
   constexpr int ES = BF16 ? 2 : 4;
-  const int row_bytes = a.head_dim * ES, cu = row_bytes / 16, ps = a.c.page.d;
+  const int row_bytes = a.head_dim * ES, cu_log2 = 31 - __clz(row_bytes / 16), ps = a.c.page.d;   // head_dim 64 or 128
   const int Hk = a.c.n_heads, Hq = a.n_q_heads, ru = a.units.d;
   const int64_t g0 = sp.row0 + t0;
   const int nrot = (Hq + Hk) * ru, items = nt * static_cast<int>(a.per.d);
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(256, kAppendBlocks) paged_append_kernel(const 
                     : static_cast<const uint8_t*>(a.k.p) + ((g0 + it.r) * a.k.row + (it.h - Hq) * a.k.head) * ES;
       it.w = rope_unit<BF16, INTER>(src, x - it.h * ru, t.pairs);
     } else {
-      const int h = (x - nrot) / cu, o = ((x - nrot) - h * cu) * 16;
+      const int h = (x - nrot) >> cu_log2, o = ((x - nrot) - (h << cu_log2)) * 16;
       it.h = Hq + Hk + h;
       it.w = {static_cast<const uint8_t*>(a.v.p) + ((g0 + it.r) * a.v.row + h * a.v.head) * ES + o, -1, o};
     }
@@ -467,16 +467,16 @@ constexpr int kMoveDeep = 4;   // 2: 64 sequences of 1000 slots to 750 in 204 in
 constexpr int kMoveChunks = kMoveThreads * kMoveDeep;
 constexpr int kMoveMaxRows = 256;   // of a block: slices of at least 4 chunks
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int slices,
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int slices_log2,
                                                                   int blocks) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int64_t s_from[kMoveMaxRows], s_to[kMoveMaxRows];
+  __shared__ int s_from[kMoveMaxRows], s_to[kMoveMaxRows];   // pool rows, or -1
   int id = blockIdx.x;
   const int blk = id % blocks;
   id /= blocks;
-  const int slice = id % slices;
-  id /= slices;
+  const int slice = id & ((1 << slices_log2) - 1);
+  id >>= slices_log2;
   const int h = id % a.src.n_heads, l = id / a.src.n_heads, s = blockIdx.y;
   const int tid = threadIdx.x;
   const bool in_place = a.k == a.dk;
@@ -485,12 +485,19 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   bool bad;
   const int64_t L = evict_len(a, s, &bad);
   const int m = static_cast<int>(a.keep < L ? a.keep : L);
-  const int all = 2 * a.row_bytes / 16, cols = all / slices, rows = kMoveChunks / cols;
+  // The thread's chunk of a row is the same in all of its rows: tid >> cols_log2 and every row_step-th behind it.
+  const int all_log2 = 31 - __clz(2 * a.row_bytes / 16), cols_log2 = all_log2 - slices_log2;
+  const int rows = kMoveChunks >> cols_log2, row_step = kMoveThreads >> cols_log2, r0 = tid >> cols_log2;
+  const int c = (slice << cols_log2) + (tid & ((1 << cols_log2) - 1));
+  const bool is_v = (c >> (all_log2 - 1)) != 0;
+  const int64_t off = (c - (is_v ? 1 << (all_log2 - 1) : 0)) * 16;
+  const uint8_t* src = (is_v ? a.v : a.k) + l * a.src_layer_rows * a.row_bytes + off;
+  uint8_t* dst = (is_v ? a.dv : a.dk) + l * a.dst_layer_rows * a.row_bytes + off;
   const int32_t* kept = a.kept + ((static_cast<int64_t>(l) * a.src.n_seqs + s) * a.src.n_heads + h) * a.kept_stride;
   for (int i0 = blk * rows; i0 < m; i0 += blocks * rows) {
     const int nr = min(rows, m - i0);
     float w = 0.f;
-    int64_t from = -1, to = -1;
+    int from = -1, to = -1;
     if (tid < nr) {
       const int i = i0 + tid;
       from = slot_row(a.src, s, h, kept[i]);
@@ -503,26 +510,21 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     }
     __syncthreads();
     uint4 x[kMoveDeep];
+    int at[kMoveDeep];
 #pragma unroll
     for (int d = 0; d < kMoveDeep; ++d) {
-      const int e = d * kMoveThreads + tid, r = e / cols, c = slice * cols + e % cols;
+      const int r = r0 + d * row_step;
       x[d] = make_uint4(0u, 0u, 0u, 0u);
-      if (r >= nr || s_to[r] < 0 || s_from[r] < 0) continue;
-      const bool is_v = c >= all / 2;
-      x[d] = *reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + (l * a.src_layer_rows + s_from[r]) * a.row_bytes +
-                                             (is_v ? c - all / 2 : c) * 16);
+      at[d] = r < nr ? s_to[r] : -1;
+      if (at[d] < 0 || s_from[r] < 0) continue;
+      x[d] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(s_from[r]) * a.row_bytes);
     }
     if (in_place) __syncthreads();
     if (slice == 0 && to >= 0) a.dacc[l * a.dst_layer_rows + to] = w;
 #pragma unroll
-    for (int d = 0; d < kMoveDeep; ++d) {
-      const int e = d * kMoveThreads + tid, r = e / cols, c = slice * cols + e % cols;
-      if (r >= nr || s_to[r] < 0) continue;
-      const bool is_v = c >= all / 2;
-      *reinterpret_cast<uint4*>((is_v ? a.dv : a.dk) + (l * a.dst_layer_rows + s_to[r]) * a.row_bytes +
-                                (is_v ? c - all / 2 : c) * 16) = x[d];
-    }
-    __syncthreads();   // s_from and s_to are rewritten
+    for (int d = 0; d < kMoveDeep; ++d)
+      if (at[d] >= 0) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(at[d]) * a.row_bytes) = x[d];
+    if (blocks * rows < m - i0) __syncthreads();   // s_from and s_to are rewritten
   }
   if (blockIdx.x == 0 && tid == 0) {
     if (a.dst_pos != a.src_pos) a.dst_pos[s] = a.src_pos[s];
@@ -607,18 +609,18 @@ cudaError_t launch_paged_evict(const Launch& L, const EvictArgs& a) {
   // slice's blocks, so slices (of at least 64 bytes) are cut until there are
   // about four CTAs for each SM.
   const int all = 2 * a.row_bytes / 16;
-  int slices = 1;
+  int slices_log2 = 0;
   int64_t blocks = 1;
   if (a.k == a.dk) {
-    while (all / slices > 4 && nl * H * S * slices < 4 * L.sm_count) slices *= 2;
+    while (all >> slices_log2 > 4 && (nl * H * S << slices_log2) < 4 * L.sm_count) ++slices_log2;
   } else {
     const int rows = kMoveChunks / all;
     blocks = (a.keep + rows - 1) / rows;
     const int64_t most = (1ll << 30) / (nl * H);   // the grid's x dimension
     blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
   }
-  return launch_kernel(evict_move_kernel, dim3(static_cast<unsigned>(nl * H * slices * blocks), static_cast<unsigned>(S)),
-                       dim3(kMoveThreads), 0, L.stream, a, slices, static_cast<int>(blocks));
+  return launch_kernel(evict_move_kernel, dim3(static_cast<unsigned>((nl * H << slices_log2) * blocks), static_cast<unsigned>(S)),
+                       dim3(kMoveThreads), 0, L.stream, a, slices_log2, static_cast<int>(blocks));
 }
 
 }  // namespace vx

@@ -72,10 +72,10 @@ PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_head
     }
   }
   p.splits = static_cast<int>(sp < 1 ? 1 : sp);
-  // Sum of the weights: segments until there are a few CTAs for each place on the SMs (8 of 128 threads each), none
+  // Sum of the weights: segments until there are about six CTAs for each place on the SMs (4 of 128 threads each), none
   // below four blocks of 64 rows.
-  const int64_t w_ctas = lanes * ((max_kv + 63) / 64), most_segs = rows / 256;
-  int64_t segs = (3 * 8 * kPlanSms + w_ctas - 1) / w_ctas;
+  const int64_t w_ctas = lanes * ((max_kv + 127) / 128), most_segs = rows / 256;
+  int64_t segs = (24 * kPlanSms + w_ctas - 1) / w_ctas;
   if (segs > most_segs) segs = most_segs;
   if (segs > 32) segs = 32;
   p.w_segs = static_cast<int>(segs < 1 ? 1 : segs);

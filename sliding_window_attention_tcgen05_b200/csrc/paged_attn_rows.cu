@@ -891,16 +891,19 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine_kernel(con
 
 // ---------------------------------------------------------------- weights --
 // Accumulated weights: acc_j = decay * acc_j + sum over the chunk's rows of
-// exp(s - lse).  The keys are the M side (K fragments stay in registers), the
-// rows stream past in blocks of 64, so every slot's sum stays in one thread
-// group's registers: no atomics, a fixed order.  CTA per (64 slots x segment
+// exp(s - lse).  The keys are the M side (32 a warp, whose K fragments stay in
+// registers), the rows stream past in blocks of 64, so every slot's sum stays in
+// one thread group's registers: no atomics, a fixed order.  With 16 keys a warp
+// each Q fragment read fed one product (4 chunks of 1000 tokens over 3000, 32/8
+// heads of 128: 299 us, shared memory and mma pipe both under half busy).  CTA
+// per (128 slots x segment
 // of their row blocks, K/V head, sequence): early slots are seen by all rows
 // and late ones by few, and cutting the rows into segments evens that out (8
 // ragged chunks of 1500 tokens, 12 heads: 465 us without segments).  Segments'
 // sums go to the workspace and are added up by paged_attn_weights_sum_kernel.
 // Slots from part_stride on (a caller's max_kv that was too low) are left to
 // the first segment, which then takes all their rows.
-constexpr int kWKeys = 64;
+constexpr int kWKeys = 128;
 constexpr int kWRows = 64;
 
 // acc of slot j's row: decay * acc + x.
@@ -912,14 +915,14 @@ __device__ __forceinline__ float* weight_part(const PagedAttnArgs& a, int seg, i
 }
 
 template <int D, bool MOD>
-__global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_constant__ PagedAttnArgs a) {
+__global__ void __launch_bounds__(128, D == 128 ? 4 : 5) paged_attn_weights_kernel(const __grid_constant__ PagedAttnArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int CPR = D / 8;
-  extern __shared__ __align__(128) uint8_t smem[];   // K tile, two Q blocks of 64 rows, their places
-  const uint32_t sk = smem_addr(smem);
-  const uint32_t sq0 = sk + kWKeys * 2 * D;
-  float* s_lse = reinterpret_cast<float*>(smem + (kWKeys + 2 * kWRows) * 2 * D);   // [2][64]
+  static_assert(kWKeys == 2 * kWRows, "the K tile passes through the Q blocks' buffers");
+  extern __shared__ __align__(128) uint8_t smem[];   // two Q blocks of 64 rows (before them the K tile), their places
+  const uint32_t sq0 = smem_addr(smem);
+  float* s_lse = reinterpret_cast<float*>(smem + 2 * kWRows * 2 * D);             // [2][64]
   float* s_sl = s_lse + 2 * kWRows;                                               // [2][64]
   int* s_i = reinterpret_cast<int*>(s_sl + 2 * kWRows);                           // [2][64]: i - first slot of the tile
   const int kh = blockIdx.y, s = blockIdx.z;
@@ -967,34 +970,38 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
       cp_async_commit();
     };
     const int blocks = (rz - ra + kWRows - 1) / kWRows;
+    uint32_t ka[2][D / 16][4];   // this warp's 2 x 16 keys as A fragments
     if (blocks > 0) {
       for (int i = tid; i < kWKeys * CPR; i += 128) {
         const int r = i / CPR, c = i % CPR;
         const int gr = j0 + r < j1 ? slot_row(a.c, s, kh, j0 + r) : -1;
-        cp_async16(sk + r * 2 * D + ((c ^ (r & 7)) << 4), kp + static_cast<int64_t>(max(gr, 0)) * D + c * 8, gr >= 0);
+        cp_async16(sq0 + r * 2 * D + ((c ^ (r & 7)) << 4), kp + static_cast<int64_t>(max(gr, 0)) * D + c * 8, gr >= 0);
       }
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncthreads();
+#pragma unroll
+      for (int mk = 0; mk < 2; ++mk) {   // ldmatrix x4 = rows 0-7 / 8-15 at dims 0-7 / 8-15
+        const int r = warp * 32 + mk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          ldsm_x4(sq0 + r * 2 * D + (((ks * 2 + (lane >> 4)) ^ (r & 7)) << 4), ka[mk][ks][0], ka[mk][ks][1],
+                  ka[mk][ks][2], ka[mk][ks][3]);
+      }
+      __syncthreads();
       stage_q(0, 0);
     }
-    cp_async_wait<0>();
-    __syncthreads();
-    // This warp's 16 keys as A fragments: ldmatrix x4 = rows 0-7 / 8-15 at dims 0-7 / 8-15.
-    uint32_t ka[D / 16][4];
-    {
-      const int r = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+    int jr[2][2];   // this thread's keys, from j0
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        ldsm_x4(sk + r * 2 * D + (((ks * 2 + (lane >> 4)) ^ (r & 7)) << 4), ka[ks][0], ka[ks][1], ka[ks][2], ka[ks][3]);
-    }
-    const int jr[2] = {warp * 16 + (lane >> 2), warp * 16 + (lane >> 2) + 8};   // from j0
-    const float jf[2] = {static_cast<float>(jr[0]), static_cast<float>(jr[1])};
+    for (int mk = 0; mk < 2; ++mk)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) jr[mk][half] = warp * 32 + mk * 16 + half * 8 + (lane >> 2);
     const int pr = pre - j0;
-    float sum[2] = {0.f, 0.f};
+    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
     for (int blk = 0; blk < blocks; ++blk) {
       const int buf = blk & 1;
-      if (blk > 0) {
-        cp_async_wait<0>();
-        __syncthreads();
-      }
+      cp_async_wait<0>();
+      __syncthreads();
       if (blk + 1 < blocks) stage_q(blk + 1, buf ^ 1);
       const uint32_t sq = sq0 + buf * kWRows * 2 * D;
       // Whether all rows of the block see all keys of the tile.
@@ -1003,44 +1010,51 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
       const int i_last = q.old + static_cast<int>(a.group_div.div(r_last)) - j0;
       const bool clean = (i_first >= kWKeys - 1 && i_last - a.window < 0) || pr >= kWKeys;
       auto rows8 = [&](int nb, auto masked) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};   // keys jr[0] (0, 1) and jr[1] (2, 3), rows col, col + 1
+        float c[2][4] = {};   // of each 16 keys: jr[0] (0, 1) and jr[1] (2, 3), rows col, col + 1
         const int r = nb * 8 + (lane & 7);
 #pragma unroll
         for (int h = 0; h < D / 32; ++h) {
           uint32_t b0, b1, b2, b3;
           ldsm_x4(sq + r * 2 * D + (((h * 4 + (lane >> 3)) ^ (r & 7)) << 4), b0, b1, b2, b3);
-          mma_bf16_16816(c, ka[2 * h][0], ka[2 * h][1], ka[2 * h][2], ka[2 * h][3], b0, b1);
-          mma_bf16_16816(c, ka[2 * h + 1][0], ka[2 * h + 1][1], ka[2 * h + 1][2], ka[2 * h + 1][3], b2, b3);
+#pragma unroll
+          for (int mk = 0; mk < 2; ++mk) {
+            mma_bf16_16816(c[mk], ka[mk][2 * h][0], ka[mk][2 * h][1], ka[mk][2 * h][2], ka[mk][2 * h][3], b0, b1);
+            mma_bf16_16816(c[mk], ka[mk][2 * h + 1][0], ka[mk][2 * h + 1][1], ka[mk][2 * h + 1][2], ka[mk][2 * h + 1][3],
+                           b2, b3);
+          }
         }
         const int col = buf * kWRows + nb * 8 + (lane & 3) * 2;
         const float2 z = *reinterpret_cast<const float2*>(s_lse + col);
-        if constexpr (MOD) {
-          scale_scores(sm, c);
-          if (sm.bias) {
-            const float2 sl = *reinterpret_cast<const float2*>(s_sl + col);
-            const int2 i = *reinterpret_cast<const int2*>(s_i + col);
-            const float i0 = static_cast<float>(i.x), i1 = static_cast<float>(i.y);
-            c[0] = fmaf(-sl.x, fabsf(i0 - jf[0]), c[0]);
-            c[1] = fmaf(-sl.y, fabsf(i1 - jf[0]), c[1]);
-            c[2] = fmaf(-sl.x, fabsf(i0 - jf[1]), c[2]);
-            c[3] = fmaf(-sl.y, fabsf(i1 - jf[1]), c[3]);
-          }
-        }
-        const float sc = MOD ? 1.f : sm.sl2;
+        const int2 i = *reinterpret_cast<const int2*>(s_i + col);
+        if constexpr (MOD) scale_scores(sm, reinterpret_cast<float(&)[8]>(c));
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float p0 = ex2_approx(fmaf(c[2 * half], sc, -z.x)), p1 = ex2_approx(fmaf(c[2 * half + 1], sc, -z.y));
-          if constexpr (decltype(masked)::value) {
-            const int2 i = *reinterpret_cast<const int2*>(s_i + col);
-            const int j = jr[half];
-            p0 = (j < pr || (j <= i.x && j > i.x - a.window)) ? p0 : 0.f;
-            p1 = (j < pr || (j <= i.y && j > i.y - a.window)) ? p1 : 0.f;
+        for (int mk = 0; mk < 2; ++mk) {
+          if constexpr (MOD) {
+            if (sm.bias) {
+              const float2 sl = *reinterpret_cast<const float2*>(s_sl + col);
+              const float i0 = static_cast<float>(i.x), i1 = static_cast<float>(i.y);
+              const float ja = static_cast<float>(jr[mk][0]), jb = ja + 8.f;
+              c[mk][0] = fmaf(-sl.x, fabsf(i0 - ja), c[mk][0]);
+              c[mk][1] = fmaf(-sl.y, fabsf(i1 - ja), c[mk][1]);
+              c[mk][2] = fmaf(-sl.x, fabsf(i0 - jb), c[mk][2]);
+              c[mk][3] = fmaf(-sl.y, fabsf(i1 - jb), c[mk][3]);
+            }
           }
-          sum[half] += p0 + p1;
+          const float sc = MOD ? 1.f : sm.sl2;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float p0 = ex2_approx(fmaf(c[mk][2 * half], sc, -z.x)), p1 = ex2_approx(fmaf(c[mk][2 * half + 1], sc, -z.y));
+            if constexpr (decltype(masked)::value) {
+              const int j = jr[mk][half];
+              p0 = (j < pr || (j <= i.x && j > i.x - a.window)) ? p0 : 0.f;
+              p1 = (j < pr || (j <= i.y && j > i.y - a.window)) ? p1 : 0.f;
+            }
+            sum[mk][half] += p0 + p1;
+          }
         }
       };
       if (clean) {
-#pragma unroll 4
+#pragma unroll 2
         for (int nb = 0; nb < kWRows / 8; ++nb) rows8(nb, std::false_type{});
       } else {
 #pragma unroll 2
@@ -1048,15 +1062,18 @@ __global__ void __launch_bounds__(128) paged_attn_weights_kernel(const __grid_co
       }
     }
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float x = sum[half];
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
-      if ((lane & 3) == 0 && j0 + jr[half] < j1) {
-        if (cut) weight_part(a, seg, s, kh)[j0 + jr[half]] = x;
-        else add_weight(a, slot_row(a.c, s, kh, j0 + jr[half]), x);
+    for (int mk = 0; mk < 2; ++mk)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x = sum[mk][half];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        const int j = j0 + jr[mk][half];
+        if ((lane & 3) == 0 && j < j1) {
+          if (cut) weight_part(a, seg, s, kh)[j] = x;
+          else add_weight(a, slot_row(a.c, s, kh, j), x);
+        }
       }
-    }
     __syncthreads();   // the tile's buffers are refilled
   }
 }
@@ -1305,7 +1322,7 @@ cudaError_t launch_combine(const Launch& L, const PagedAttnArgs& a) {
 
 template <int D, bool MOD>
 cudaError_t launch_weights(const Launch& L, const PagedAttnArgs& a, const dim3& grid) {
-  constexpr size_t smem = (kWKeys + 2 * kWRows) * 2 * D + 3 * 2 * kWRows * 4;
+  constexpr size_t smem = 2 * kWRows * 2 * D + 3 * 2 * kWRows * 4;
   return launch_kernel(paged_attn_weights_kernel<D, MOD>, grid, dim3(128), smem, L.stream, a);
 }
 

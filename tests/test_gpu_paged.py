@@ -497,6 +497,21 @@ def test_capped_scores_small_and_large(dtype, n, D, scale, cap):
     _check_attn(b, o, lse, cap=cap, track=0.0)
 
 
+@pytest.mark.parametrize("dtype,n,D,page,window,prefix", [
+    (BF, 2, 64, 16, 40, 5), (BF, 2, 128, 7, 1, 0), (BF, 3, 128, 128, 129, 70), (BF, 150, 64, 128, 40, 3),
+    (BF, 150, 128, 16, 33, 0), (BF, 150, 128, 7, 100, 61), (BF, 300, 64, 8, 1, 17), (F32, 2, 64, 16, 40, 5),
+    (F32, 6, 128, 7, 1, 0), (F32, 90, 64, 16, 33, 21)])
+def test_slots_that_no_query_sees_may_hold_anything(dtype, n, D, page, window, prefix):
+    vx = _vx()
+    b = Batch([700], [n], 4, 2, D, page, dtype, weights=True)
+    pg, off = b.slots(0, 700 - window + 1, prefix)          # between the prefix and the first query's window
+    for pool, x in ((b.cache.k, float("nan")), (b.cache.v, float("inf"))):
+        pool[0, pg.cuda(), :, off.cuda()] = x
+    o, lse = vx.paged_attn_fwd(b.cache, 0, b.q.cuda(), b.q_start, n, window=window, track=0.5, return_lse=True,
+                               prefix=torch.tensor([prefix], dtype=torch.int32).cuda())
+    _check_attn(b, o, lse, window=window, prefix=[prefix], track=0.5)
+
+
 @pytest.mark.parametrize("case", ["empty", "none"])
 def test_no_rows(case):
     vx = _vx()

@@ -123,6 +123,10 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) { 
   return ok != 0;
 }
 
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {   // no arrival
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ float ex2_ordered(float x) {   // keeps its place among the other asm statements
   float y;
   asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -259,7 +263,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           const uint32_t mine = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (lane & -lanes);
           const bool whole = (have & mine) == mine;
           const uint32_t runs = __ballot_sync(0xffffffffu, whole);     // a bit for each lane of a whole run
-          if (lane == 0) mbar_arrive_expect_tx(full, __popc(runs) * (4 * D * 2));
+          // Announced alone: lane 0 arrives like the others, after its own copies have landed (their waits and fences
+          // order no other lane's).
+          if (lane == 0) mbar_expect_tx(full, __popc(runs) * (4 * D * 2));
           __syncwarp();
           if (whole && (lane & (lanes - 1)) == 0)
 #pragma unroll
@@ -282,7 +288,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
             cp_async_wait<0>();
             fence_proxy_async_smem();
           }
-          if (lane != 0) mbar_arrive(full);
+          mbar_arrive(full);
         } else {
 #pragma unroll
           for (int k0 = 0; k0 < 128 / RPI; k0 += 8) {   // eight rows' numbers first: a shuffle before each copy takes 75 cycles a copy

@@ -45,7 +45,9 @@ struct TcCfg {
   static constexpr int kTile = kTcKeys * D * 2;               // one Q, K or V tile
   static constexpr int kStages = D == 128 ? 5 : 8;            // ring of K / V tiles
   static constexpr int kLag = 1;                              // a producer's cp.async tiles in flight behind the newest
-  static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024 + 256;
+  static constexpr int kBars = 2 * kStages + 19;              // mbarriers of the CTA
+  static constexpr int kTail = (kBars + 1) * 8;               // behind the tiles: the barriers, the TMEM address, the abort flag
+  static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024 + kTail;   // 1024: the tiles' alignment
 };
 
 struct TcItem {
@@ -152,6 +154,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + NST * TILE);
   // TK: the turns of warp w of each warpgroup at their scheduler's MUFU.
   constexpr int FULL = 0, EMPTY = NST, SF = 2 * NST, PF = SF + 2, PVD = PF + 4, DR = PVD + 2, TK = DR + 2, QF = TK + 8, NBAR = QF + 1;
+  static_assert(NBAR == Cfg::kBars && NBAR * 8 + 8 <= Cfg::kTail, "shared memory behind the tiles");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_addr(bars + i); };

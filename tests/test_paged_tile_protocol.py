@@ -86,3 +86,19 @@ def test_the_kernels_producer_announces_without_arriving():
     assert "mbar_expect_tx(full" in body and "arrive_expect_tx" not in body
     assert re.findall(r"[^\n]*mbar_arrive\(full\);", body) == ["          mbar_arrive(full);"]   # every lane, after its wait
     assert body.index("cp_async_wait<0>()") < body.index("mbar_arrive(full)")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_barriers_fit_behind_the_tiles(D):
+    # The dynamic shared memory may start on any 16-byte boundary, so the 1024 bytes for the tiles' alignment are no room.
+    src = open(os.path.join(ROOT, "sliding_window_attention_tcgen05_b200", "csrc", "paged_attn_tc.cu")).read()
+    names = dict(NST=int(re.search(r"kStages = D == 128 \? (\d+) : (\d+)", src)[1 if D == 128 else 2]), kTile=256 * D)
+    names["kStages"] = names["NST"]
+    for part in re.search(r"constexpr int (FULL = 0.*?);", src)[1].split(","):
+        name, value = part.split("=")
+        names[name.strip()] = eval(value, {}, names)
+    for name in ("kBars", "kTail", "kSmem"):
+        if found := re.search(rf"constexpr int {name} = (.*?);", src):
+            names[name] = eval(found[1], {}, names)
+    tiles = (2 + names["NST"]) * names["kTile"]
+    assert tiles + 1008 + names["NBAR"] * 8 + 8 <= names["kSmem"] <= 227 * 1024

@@ -126,11 +126,6 @@ __device__ __forceinline__ ScoreMod score_mod(const PagedAttnArgs& a) {
   m.bias = a.slopes != nullptr;
   return m;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either is
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 // N raw scores.
 template <int N>
 __device__ __forceinline__ void scale_scores(const ScoreMod& m, float (&s)[N]) {
@@ -151,14 +146,15 @@ __device__ __forceinline__ void scale_scores(const ScoreMod& m, float (&s)[N]) {
         f2_unpack(fmul2(fmul2(x, sl), p), s[e], s[e + 1]);
       }
     } else {   // two at a time: 1 / a and 1 / b from one reciprocal of a b (exponents up to 2^60, beyond which tanh is 1
-               // to the last bit, so that the product stays finite)
+               // to the last bit, so that the product stays finite; a NaN counts as such a one in it and stays its own
+               // score's, since the mask may hide it from a row that sees its partner)
 #pragma unroll
       for (int e = 0; e < N; e += 2) {
-        const float a = ex2_approx(min_nan(s[e] * m.two_z, 60.f)) + 1.f;
-        const float b = ex2_approx(min_nan(s[e + 1] * m.two_z, 60.f)) + 1.f;
+        const float x = s[e] * m.two_z, y = s[e + 1] * m.two_z;
+        const float a = ex2_approx(fminf(x, 60.f)) + 1.f, b = ex2_approx(fminf(y, 60.f)) + 1.f;
         const float r = -2.f * m.cap2 * rcp_approx(a * b);
-        s[e] = fmaf(r, b, m.cap2);
-        s[e + 1] = fmaf(r, a, m.cap2);
+        s[e] = x != x ? x : fmaf(r, b, m.cap2);
+        s[e + 1] = y != y ? y : fmaf(r, a, m.cap2);
       }
     }
   } else {

@@ -1,0 +1,67 @@
+"""GPU tests of the paged-cache operators' corners, against the same float64
+statement and with the same tolerances as test_gpu_paged.py."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged as paged
+from test_gpu_paged import BF, F32, U, Batch, _check_attn, _host, _randn, _vx, _within
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------- non-finite keys and queries
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,D", [(2, 64), (2, 128), (6, 64), (12, 128), (150, 64), (150, 128)])
+@pytest.mark.parametrize("cap", [0.0, 2.0, 1e4])
+@pytest.mark.parametrize("kind", ["nan", "inf", "one inf"])
+def test_a_key_that_is_not_finite_reaches_no_query_that_does_not_see_it(dtype, n, D, cap, kind):
+    # The last token's key, V finite: the tokens before it do not see it.  Scores far above the cap of 2, far below 1e4.
+    vx = _vx()
+    b = Batch([140, 9], [n, n], 4, 2, D, 16, dtype, scale=8.0, weights=True)
+    for s, old in enumerate(b.olds):
+        at = slice(0, 1) if kind == "one inf" else slice(None)
+        x = float("nan") if kind == "nan" else float("inf")
+        b.k[s][0, -1, :, at] = x
+        pg, off = b.slots(s, old + n, old + n - 1)
+        b.cache.k[0, pg.cuda(), :, off.cuda(), at] = x
+    o, lse = vx.paged_attn_fwd(b.cache, 0, b.q.cuda(), b.q_start, n, cap=cap, track=0.0, return_lse=True)
+    with np.errstate(invalid="ignore"):
+        for s, old in enumerate(b.olds):
+            rows = slice(b.starts[s], b.starts[s] + n - 1)     # without the last token: nothing is off there
+            r = paged.attention(_host(b.q)[rows], _host(b.k[s][0])[:-1], _host(b.v[s][0])[:-1], old, cap=cap)
+            ds = ((D + 8) * r["smax"]) * U + cap * 2.0 ** -21
+            rel = 2 * (ds + 2.0 ** -21) + (old + n + 8) * U + (2.0 ** -8 if dtype == BF else 0.0)
+            tol = r["absv"] * rel[..., None] * 1.01 + (2.0 ** -8 if dtype == BF else 2 * U) * np.abs(r["o"]) + 1e-30
+            _within(_host(o)[rows], r["o"], tol, f"o of sequence {s}")
+            dz = ds + 2.0 ** -20 + (old + n + 8) * U + 4 * U * np.abs(r["lse"])
+            _within(_host(lse)[rows], r["lse"], dz, f"lse of sequence {s}")
+            last = b.starts[s] + n - 1
+            if kind != "one inf":                              # inf - inf, or NaN: the query that sees it passes it on
+                assert torch.isnan(o[last]).all() and torch.isnan(lse[last]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,D", [(12, 128), (18, 64), (150, 64), (150, 128)])
+@pytest.mark.parametrize("cap", [0.0, 2.0])
+@pytest.mark.parametrize("hq", [4, 2])
+def test_a_query_that_is_not_finite_leaves_the_weights_of_slots_it_does_not_see(dtype, n, D, cap, hq):
+    # One head of one token is NaN, under a window: the slots after it and before its window, and the other K/V head.
+    vx = _vx()
+    old, window, t = 140, 40, n // 2 - 1
+    b = Batch([old], [n], hq, 2, D, 16, dtype, scale=8.0, weights=True)
+    q = b.q.clone()
+    q[t, 0] = float("nan")
+    o, lse = vx.paged_attn_fwd(b.cache, 0, q.cuda(), b.q_start, n, window=window, cap=cap, track=0.0, return_lse=True)
+    assert torch.isnan(o[t, 0]).all() and torch.isnan(lse[t, 0])
+    assert not torch.isnan(o[t, 1:]).any() and not torch.isnan(lse[t, 1:]).any()
+    r = paged.attention(_host(b.q), _host(b.k[0][0]), _host(b.v[0][0]), old, window=window, cap=cap)
+    ds = ((D + 8) * r["smax"]) * U + cap * 2.0 ** -21
+    dz = ds + 2.0 ** -20 + (old + n + 8) * U + 4 * U * np.abs(r["lse"])
+    rel = ds.max() + dz.max() + 2.0 ** -20 + n * 2 * U
+    got = _host(b.gather(b.cache.acc, 0, old + n))[0].T
+    seen = paged.seen(old, n, window)[t]
+    want = r["weights"].copy()                                 # a hidden slot has no part of the query's in it
+    want[0, seen] = np.nan
+    _within(got, want, 1.01 * r["weights"] * rel + 4 * U * r["weights"] + 1e-30, "weights")

@@ -1089,6 +1089,7 @@ paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a, int bloc
   pdl_wait();
   pdl_trigger();
   __shared__ float s_lse[8];
+  __shared__ int s_i[8];   // slots of the rows' tokens
   __shared__ float part[kCombineThreads / 32][D];
   const int kh = blockIdx.y, s = blockIdx.z;
   const SeqSpan q = seq_span(a.c, a.ch, s);
@@ -1114,6 +1115,7 @@ paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a, int bloc
       z = z == -INFINITY ? INFINITY : z * kLog2e;
     }
     s_lse[warp] = z;
+    s_i[warp] = q.old + a.group_div.div(warp);
   }
   __syncthreads();
   const KeyList kl = key_list(q.old, q.old + q.n - 1, a.window, a.prefix ? a.prefix[s] : 0, q.kv);
@@ -1124,7 +1126,11 @@ paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a, int bloc
     float sum = 0.f;
     if (x >= (j < kl.cut ? 0 : kl.cut) && x < kl.total) {
       if (x < a.score_stride) {
-        for (int r = 0; r < rows; ++r) sum += ex2_approx(kept[r * a.score_stride + x] - s_lse[r]);
+        for (int r = 0; r < rows; ++r) {
+          const float w = ex2_approx(kept[r * a.score_stride + x] - s_lse[r]);
+          const int i = s_i[r];
+          sum += j < kl.pre || (j <= i && j > i - a.window) ? w : 0.f;   // a row whose sum is NaN gives none to what it does not see
+        }
       } else if (row >= 0) {   // the caller's max_kv was too low: the product again
         const ScoreMod sm = score_mod(a);
         for (int r = 0; r < rows; ++r) {

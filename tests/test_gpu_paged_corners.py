@@ -43,7 +43,7 @@ def test_a_key_that_is_not_finite_reaches_no_query_that_does_not_see_it(dtype, n
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("n,D", [(12, 128), (18, 64), (150, 64), (150, 128)])
+@pytest.mark.parametrize("n,D", [(2, 64), (2, 128), (4, 64), (12, 128), (18, 64), (150, 64), (150, 128)])
 @pytest.mark.parametrize("cap", [0.0, 2.0])
 @pytest.mark.parametrize("hq", [4, 2])
 def test_a_query_that_is_not_finite_leaves_the_weights_of_slots_it_does_not_see(dtype, n, D, cap, hq):

@@ -52,16 +52,22 @@ def _p(t):
     return C.c_void_p(t.data_ptr())
 
 
+_STATUS_BYTES = 256    # the status word's part of a workspace, at its start
+
+
 class Workspace:
-    """A device scratch buffer; grows on demand, never shrinks."""
+    """A device scratch buffer; grows on demand, never shrinks.  What calls recorded in its status word stays when it
+    grows (of calls on the stream that is current then, or that the host has waited for)."""
 
     def __init__(self, nbytes: int = 0, device=None):
         self.device = torch.device(device or "cuda")
-        self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        self.buf = torch.zeros(max(nbytes, _STATUS_BYTES), dtype=torch.uint8, device=self.device)
 
     def get(self, nbytes: int):
         if self.buf.numel() < nbytes:
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            buf[:_STATUS_BYTES].copy_(self.buf[:_STATUS_BYTES])
+            self.buf = buf
         return C.c_void_p(self.buf.data_ptr()), C.c_size_t(self.buf.numel())
 
     def ptr(self):

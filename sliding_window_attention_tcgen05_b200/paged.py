@@ -16,7 +16,7 @@ from dataclasses import dataclass, fields
 import torch
 
 from ._lib import VxPagedCache, VxRopeCfg, lib
-from .api import Workspace
+from .api import _STATUS_BYTES, Workspace
 
 try:
     from . import _bind
@@ -25,7 +25,6 @@ except ImportError as e:
                       "`python sliding_window_attention_tcgen05_b200/build.py`") from e
 
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-_STATUS_BYTES = 256    # a workspace that only holds the status word
 
 
 def _ws(ws: Workspace | None, nbytes: int, device: int):

@@ -65,3 +65,20 @@ def test_a_query_that_is_not_finite_leaves_the_weights_of_slots_it_does_not_see(
     want = r["weights"].copy()                                 # a hidden slot has no part of the query's in it
     want[0, seen] = np.nan
     _within(got, want, 1.01 * r["weights"] * rel + 4 * U * r["weights"] + 1e-30, "weights")
+
+
+# ------------------------------------------------------- status and scratch
+
+def test_a_full_table_is_still_reported_after_the_workspace_has_grown():
+    vx = _vx()
+    b = Batch([30], [4], 2, 2, 64, 16, BF, weights=True)
+    c = vx.PagedCache(1, b.cache.k.shape[1], 16, 2, 64, 1, 2, weights=True)      # 32 slots: two tokens too many
+    c.table.copy_(b.cache.table[:, :2])
+    c.lens.copy_(b.cache.lens)
+    ws = vx.Workspace(256)
+    vx.status_reset(ws)
+    k = _randn((4, 2, 64), BF, torch.Generator().manual_seed(1)).cuda()
+    vx.paged_append(c, 0, k, k, b.q_start, 4, ws=ws)
+    c.lens.fill_(28)                                                            # nothing wrong from here on
+    vx.paged_attn_fwd(c, 0, b.q.cuda(), b.q_start, 4, track=0.0, ws=ws)
+    assert ws.buf.numel() > 256 and vx.status_check(ws) == 1

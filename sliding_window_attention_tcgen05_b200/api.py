@@ -52,22 +52,36 @@ def _p(t):
     return C.c_void_p(t.data_ptr())
 
 
+def _capturing(t) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 _STATUS_BYTES = 256    # the status word's part of a workspace, at its start
 
 
 class Workspace:
     """A device scratch buffer; grows on demand, never shrinks.  What calls recorded in its status word stays when it
-    grows (of calls on the stream that is current then, or that the host has waited for)."""
+    grows (of calls on the stream that is current then, or that the host has waited for).  A buffer that calls were
+    captured with is kept for their replays when a larger one takes its place; grown inside a capture, every replay
+    sets the status word back to what it was."""
 
     def __init__(self, nbytes: int = 0, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = torch.zeros(max(nbytes, _STATUS_BYTES), dtype=torch.uint8, device=self.device)
+        self._captured = False     # a captured graph may hold buf's address
+        self._kept = []            # buffers that captured graphs may hold
 
     def get(self, nbytes: int):
+        capturing = _capturing(self.buf)
         if self.buf.numel() < nbytes:
             buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
             buf[:_STATUS_BYTES].copy_(self.buf[:_STATUS_BYTES])
-            self.buf = buf
+            if capturing or self._captured:
+                self._kept.append(self.buf)
+            elif self.buf.is_cuda:      # calls in flight on a stream that is not the buffer's own
+                self.buf.record_stream(torch.cuda.current_stream(self.device))
+            self.buf, self._captured = buf, False
+        self._captured |= capturing
         return C.c_void_p(self.buf.data_ptr()), C.c_size_t(self.buf.numel())
 
     def ptr(self):

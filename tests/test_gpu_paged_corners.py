@@ -82,3 +82,28 @@ def test_a_full_table_is_still_reported_after_the_workspace_has_grown():
     c.lens.fill_(28)                                                            # nothing wrong from here on
     vx.paged_attn_fwd(c, 0, b.q.cuda(), b.q_start, 4, track=0.0, ws=ws)
     assert ws.buf.numel() > 256 and vx.status_check(ws) == 1
+
+
+def test_a_captured_workspace_is_not_handed_out_again_when_it_grows():
+    vx = _vx()
+    b = Batch([300, 45], [40, 40], 4, 2, 64, 16, BF, weights=True)
+    q, ws = b.q.cuda(), vx.Workspace(256)
+    call = lambda: vx.paged_attn_fwd(b.cache, 0, q, b.q_start, 40, max_kv=b.max_kv, track=0.0, return_lse=True, ws=ws)
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        want = [t.clone() for t in call()] + [b.cache.acc.clone()]
+    st.synchronize()
+    size, at = ws.buf.numel(), ws.buf.data_ptr()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        out = call()
+    ws.get(4 * size)
+    others = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert at not in [t.data_ptr() for t in others]
+    b.cache.acc.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in others)
+    for x, y in zip([*out, b.cache.acc], want):
+        assert torch.equal(x.nan_to_num(), y.nan_to_num())

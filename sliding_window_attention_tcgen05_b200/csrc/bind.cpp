@@ -133,12 +133,30 @@ struct Scratch {
 };
 
 // The tensors of a paged cache and their C description, checked when it is
-// made and again when a storage has moved.
+// made and again when a tensor has changed in place (moved, resized, another
+// view of its storage).
 struct Cache {
   Tensor k, v, table, lens, pos;
   OptTensor acc;
   vx_paged_cache c{};
   int dev = 0;
+  struct Seen {
+    const void* p;
+    std::array<int64_t, 5> size;
+    int64_t dim;
+    at::ScalarType dt;
+    bool operator==(const Seen& o) const { return p == o.p && size == o.size && dim == o.dim && dt == o.dt; }
+  };
+  std::array<Seen, 6> seen{};   // the tensors as described
+
+  static Seen look(const Tensor& t) {
+    Seen s{t.data_ptr(), {}, t.is_contiguous() ? t.dim() : -1, t.scalar_type()};
+    for (int64_t i = 0; i < t.dim() && i < 5; ++i) s.size[i] = t.size(i);
+    return s;
+  }
+  std::array<Seen, 6> look() const {
+    return {look(k), look(v), look(table), look(lens), look(pos), acc ? look(*acc) : Seen{}};
+  }
 
   Cache(Tensor k_, Tensor v_, OptTensor acc_, Tensor table_, Tensor lens_, Tensor pos_)
       : k(std::move(k_)), v(std::move(v_)), table(std::move(table_)), lens(std::move(lens_)), pos(std::move(pos_)),
@@ -167,11 +185,10 @@ struct Cache {
     c.head_dim = narrow(D);
     c.n_seqs = narrow(S);
     c.max_pages = narrow(table.size(1));
+    seen = look();
   }
   const vx_paged_cache* fresh() {
-    if (c.k != k.data_ptr() || c.v != v.data_ptr() || c.table != table.data_ptr() || c.lens != lens.data_ptr() ||
-        c.pos != pos.data_ptr() || (acc && c.acc != acc->data_ptr()))
-      describe();
+    if (!(look() == seen)) describe();
     return &c;
   }
 };

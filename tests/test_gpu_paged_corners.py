@@ -107,3 +107,29 @@ def test_a_captured_workspace_is_not_handed_out_again_when_it_grows():
     assert not any(t.any() for t in others)
     for x, y in zip([*out, b.cache.acc], want):
         assert torch.equal(x.nan_to_num(), y.nan_to_num())
+
+
+def test_tensors_resized_in_place_are_described_again():
+    # Host side only: nothing is launched on the old description.
+    vx = _vx()
+    make = lambda: vx.PagedCache(2, 8, 16, 2, 64, 3, 4, weights=True, device="cuda")
+    c = make()
+    assert (c.c().n_seqs, c.c().max_pages, c.c().n_pages) == (3, 4, 8)
+    c.table.resize_(3, 2)
+    assert c.c().max_pages == 2
+    c.table.resize_(2, 2), c.lens.resize_(2), c.pos.resize_(2)
+    assert c.c().n_seqs == 2
+    for name in ("k", "v"):
+        getattr(c, name).resize_(2, 5, 2, 16, 64)
+    c.acc.resize_(2, 5, 2, 16)
+    assert c.c().n_pages == 5
+    for change, word in ((lambda c: c.lens.resize_(2), "lens"), (lambda c: c.pos.resize_(0), "pos"),
+                         (lambda c: c.v.resize_(2, 5, 2, 16, 64), "k and v"), (lambda c: c.acc.resize_(2), "acc"),
+                         (lambda c: c.table.t_(), "contiguous"), (lambda c: c.table.resize_(12), "table")):
+        c = make()
+        c.c()
+        change(c)
+        with pytest.raises(ValueError, match=word):
+            c.c()
+        with pytest.raises(ValueError, match=word):
+            vx.paged_advance(c, torch.zeros(4, dtype=torch.int32, device="cuda"), 0, 0)

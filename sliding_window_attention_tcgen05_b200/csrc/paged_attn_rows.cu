@@ -1120,6 +1120,7 @@ paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a, int bloc
   __syncthreads();
   const KeyList kl = key_list(q.old, q.old + q.n - 1, a.window, a.prefix ? a.prefix[s] : 0, q.kv);
   const float* kept = a.scores + (static_cast<int64_t>(s) * a.c.n_heads + kh) * cap * a.score_stride;
+  auto weight = [](float y) { return BF16 ? ex2_approx(y) : exp2f(y); };
   for (int j = blockIdx.x * kCombineThreads + threadIdx.x; j < q.kv; j += blocks * kCombineThreads) {
     const int x = j < kl.cut ? j : j - kl.shift;
     const int row = slot_row(a.c, s, kh, j);
@@ -1127,7 +1128,7 @@ paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a, int bloc
     if (x >= (j < kl.cut ? 0 : kl.cut) && x < kl.total) {
       if (x < a.score_stride) {
         for (int r = 0; r < rows; ++r) {
-          const float w = ex2_approx(kept[r * a.score_stride + x] - s_lse[r]);
+          const float w = weight(kept[r * a.score_stride + x] - s_lse[r]);
           const int i = s_i[r];
           sum += j < kl.pre || (j <= i && j > i - a.window) ? w : 0.f;   // a row whose sum is NaN gives none to what it does not see
         }
@@ -1142,7 +1143,7 @@ paged_attn_weights_kept_kernel(const __grid_constant__ PagedAttnArgs a, int bloc
             dot = BF16 ? fmaf(bf16_to_f(static_cast<const uint16_t*>(a.q.p)[qe + d]),
                               bf16_to_f(static_cast<const uint16_t*>(a.k)[ke + d]), dot)
                        : fmaf(static_cast<const float*>(a.q.p)[qe + d], static_cast<const float*>(a.k)[ke + d], dot);
-          sum += ex2_approx(score2(sm, dot, a.slopes ? a.slopes[h] * kLog2e : 0.f, i - j) - s_lse[r]);
+          sum += weight(score2(sm, dot, a.slopes ? a.slopes[h] * kLog2e : 0.f, i - j) - s_lse[r]);
         }
       }
     }

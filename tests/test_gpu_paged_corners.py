@@ -67,6 +67,29 @@ def test_a_query_that_is_not_finite_leaves_the_weights_of_slots_it_does_not_see(
     _within(got, want, 1.01 * r["weights"] * rel + 4 * U * r["weights"] + 1e-30, "weights")
 
 
+# ------------------------------------------------------------ fp32 throughout
+
+@pytest.mark.parametrize("n,hq,kv", [(1, 2, 0), (1, 2, 16), (4, 4, 0), (12, 2, 0), (70, 4, 0)])
+def test_fp32_weights_below_the_smallest_normal_number_are_not_flushed(n, hq, kv):
+    # Scores 0 and -92: a weight of exp(-92) = 1.1e-40.
+    vx = _vx()
+    old, D = 40, 64
+    b = Batch([old], [n], hq, 2, D, 16, F32, weights=True)
+    k, q = torch.zeros(old + n, 2, D), torch.zeros(n, hq, D)
+    k[1:old, :, 0] = -92.0
+    k[old:, :, 0] = -500.0
+    q[..., 0] = 1.0
+    pg, off = b.slots(0, old + n)
+    b.cache.k[0, pg.cuda(), :, off.cuda()] = k.cuda()
+    vx.paged_attn_fwd(b.cache, 0, q.cuda(), b.q_start, n, max_kv=kv, scale=1.0, track=0.0)
+    got = _host(b.gather(b.cache.acc, 0, old + n))[0]
+    want = n * (hq // 2) * np.exp(-92.0)
+    # The score's rounding 92 * 2^-24 * log2 e, exp2's, and a denormal's step for each row's weight.
+    tol = want * (92 * 4 * U + 2.0 ** -20) + n * (hq // 2) * 2.0 ** -149
+    _within(got[1:old], np.full((old - 1, 2), want), tol, "weights")
+    assert not got[old:].any()
+
+
 # ------------------------------------------------------- status and scratch
 
 def test_a_full_table_is_still_reported_after_the_workspace_has_grown():

@@ -18,11 +18,22 @@ import torch
 from ._lib import VxPagedCache, VxRopeCfg, lib
 from .api import _STATUS_BYTES, Workspace
 
+
+class _NoBind:
+    """In the place of _bind.so where it cannot be loaded: the paged cache's calls raise, the rest of the package works."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_bind.so could not be loaded ({self._why}); build it with "
+                          "`python sliding_window_attention_tcgen05_b200/build.py`")
+
+
 try:
     from . import _bind
 except ImportError as e:
-    raise ImportError(f"_bind.so could not be loaded ({e}); build it with "
-                      "`python sliding_window_attention_tcgen05_b200/build.py`") from e
+    _bind = _NoBind(str(e))
 
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 

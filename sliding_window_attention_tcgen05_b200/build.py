@@ -10,17 +10,19 @@ is newer than its object) and the objects are linked into
 sliding_window_attention_tcgen05_b200/libvx.so with a static CUDA runtime.
 csrc/bind.cpp (the paged-cache wrappers' marshalling, against PyTorch's C++
 headers) becomes sliding_window_attention_tcgen05_b200/_bind.so, which calls
-into libvx.so.
+into libvx.so; it is rebuilt for another torch or Python too.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -96,13 +98,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
+def _bind_abi() -> str:
+    """What _bind.so is tied to beside its sources."""
+    return f"torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('EXT_SUFFIX')}\n"
+
+
 def build_bind(force: bool = False, verbose: bool = False) -> str:
     """_bind.so; needs libvx.so."""
     src = os.path.join(CSRC, "bind.cpp")
     hdr = os.path.getmtime(os.path.join(ROOT, "include", "vx.h"))
-    if not force and not _stale(src, BIND, hdr):
+    stamp, abi = os.path.join(BUILD, "_bind.abi"), _bind_abi()
+    built_for = open(stamp).read() if os.path.exists(stamp) else None
+    if not force and built_for == abi and not _stale(src, BIND, hdr):
         return BIND
-    import sysconfig
 
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
@@ -119,6 +127,8 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError("bind.cpp failed:\n" + p.stdout + p.stderr)
+    with open(stamp, "w") as f:
+        f.write(abi)
     return BIND
 
 

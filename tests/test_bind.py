@@ -1,4 +1,5 @@
-"""The C++ marshalling of the paged cache's wrappers: what happens without it (no GPU needed)."""
+"""The C++ marshalling of the paged cache's wrappers: its build, and what happens without it (no GPU needed)."""
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -34,3 +35,35 @@ print("fine")
 def test_the_encoders_calls_do_not_need_it():
     p = subprocess.run([sys.executable, "-c", _WITHOUT], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0 and p.stdout.strip() == "fine", p.stderr[-2000:]
+
+
+def test_it_is_rebuilt_for_another_torch(tmp_path, monkeypatch):
+    from sliding_window_attention_tcgen05_b200 import build
+    runs = []
+
+    class Ok:
+        returncode, stdout, stderr = 0, "", ""
+
+    def compiler(cmd, **kw):
+        runs.append(cmd)
+        open(build.BIND, "w").close()
+        return Ok
+
+    monkeypatch.setattr(build, "BIND", str(tmp_path / "_bind.so"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    build.build_bind()
+    build.build_bind()
+    assert len(runs) == 1
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "99.0")
+    build.build_bind()
+    build.build_bind()
+    assert len(runs) == 2
+    Ok.returncode = 1                              # a failed build is tried again
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "99.1")
+    for n in (3, 4):
+        try:
+            build.build_bind()
+        except RuntimeError:
+            pass
+        assert len(runs) == n

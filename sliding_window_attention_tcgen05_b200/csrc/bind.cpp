@@ -295,9 +295,10 @@ void paged_evict(Cache& cache, int64_t keep, int64_t recent, Cache* dst, OptTens
     d = dst->fresh();
     on_device(cache.dev, dst->k, "dst");
   }
-  if (kept && kept->numel() == 0) kept.reset();
-  auto* kp = static_cast<int32_t*>(whole(kept, "kept", at::kInt, cache.dev,
-                                         static_cast<int64_t>(c->n_layers) * c->n_seqs * c->n_kv_heads * keep));
+  const int64_t lanes = static_cast<int64_t>(c->n_layers) * c->n_seqs * c->n_kv_heads;
+  int64_t slots = -1;   // a negative keep is refused below
+  if (kept && keep >= 0 && __builtin_mul_overflow(lanes, keep, &slots)) value_error("kept cannot have that many slots");
+  auto* kp = static_cast<int32_t*>(whole(kept, "kept", at::kInt, cache.dev, slots));   // keep 0: no address, no entries
   c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(cache.dev));
   const size_t need = ws != 0 ? 0 : kp ? kStatusBytes : vx_paged_evict_workspace(c, keep);
   Scratch s(ws, ws_bytes, need, cache.dev);

@@ -156,3 +156,22 @@ def test_tensors_resized_in_place_are_described_again():
             c.c()
         with pytest.raises(ValueError, match=word):
             vx.paged_advance(c, torch.zeros(4, dtype=torch.int32, device="cuda"), 0, 0)
+
+
+# ----------------------------------------------------------------- refusals
+
+def test_a_kept_tensor_of_another_size_is_refused():
+    vx = _vx()
+    b = Batch([40, 70], [0, 0], 1, 2, 64, 16, BF, weights=True)
+    kept = lambda *shape: torch.full(shape, -7, dtype=torch.int32, device="cuda")
+    before = b.cache.lens.tolist()
+    # 4 (sequence, head) pairs times 2^62 + 1 is 4 in 64 bits, times 2^62 nothing
+    for keep, k in ((20, kept(0)), (20, kept(1, 2, 2, 19)), (20, kept(2, 2, 2, 20)), ((1 << 62) + 1, kept(4)),
+                    (1 << 62, kept(0)), (1 << 61, kept(0))):
+        with pytest.raises(ValueError, match="kept"):
+            vx.paged_evict(b.cache, keep, 5, kept=k)
+    with pytest.raises(vx.VxError, match="keep"):
+        vx.paged_evict(b.cache, -1, 5, kept=kept(0))
+    assert b.cache.lens.tolist() == before
+    vx.paged_evict(b.cache, 0, 5, kept=kept(1, 2, 2, 0))
+    assert b.cache.lens.tolist() == [0, 0]

@@ -91,17 +91,22 @@ vx_rows rows_of(const Tensor& t, const char* name, int64_t n, int64_t heads, int
 
 Tensor new_rows(const Tensor& like) { return at::empty(like.sizes(), like.options()); }
 
-// The storage ranges of two tensors meet.
+// Rows of two token tensors may meet: their storage ranges do, unless both have the same distance from row to row and
+// lie beside one another within it (heads of one fused row).
 bool overlap(const Tensor& a, const Tensor& b) {
   if (a.numel() == 0 || b.numel() == 0 || a.storage().data() != b.storage().data()) return false;
-  auto span = [](const Tensor& t) {
+  auto extent = [](const Tensor& t, int64_t from) {   // bytes that dims `from` on reach over
     int64_t last = 0;
-    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
-    const char* p = static_cast<const char*>(t.data_ptr());
-    return std::array<const char*, 2>{p, p + (last + 1) * t.element_size()};
+    for (int64_t i = from; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    return (last + 1) * t.element_size();
   };
-  const auto x = span(a), y = span(b);
-  return x[0] < y[1] && y[0] < x[1];
+  const char *p = static_cast<const char*>(a.data_ptr()), *q = static_cast<const char*>(b.data_ptr());
+  if (q >= p + extent(a, 0) || p >= q + extent(b, 0)) return false;
+  if (a.dim() != 3 || b.dim() != 3) return true;
+  const int64_t row = a.stride(0) * a.element_size();
+  if (row <= 0 || row != b.stride(0) * b.element_size()) return true;
+  const int64_t d = ((q - p) % row + row) % row;   // b's rows behind a's
+  return d < extent(a, 1) || d + extent(b, 1) > row;
 }
 bool same_rows(const Tensor& a, const Tensor& b) { return a.data_ptr() == b.data_ptr() && a.strides() == b.strides(); }
 

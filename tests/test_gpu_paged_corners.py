@@ -158,6 +158,33 @@ def test_tensors_resized_in_place_are_described_again():
             vx.paged_advance(c, torch.zeros(4, dtype=torch.int32, device="cuda"), 0, 0)
 
 
+# -------------------------------------------------- tensors in one fused row
+
+def test_outputs_may_be_other_heads_of_the_inputs_rows():
+    vx = _vx()
+    b = Batch([30, 9], [5, 3], 4, 2, 64, 16, BF)
+    cfg, gen = vx.RopeCfg(theta=1e4), torch.Generator().manual_seed(2)
+    row = _randn((8, 12, 64), BF, gen).cuda()
+    k, v = (_randn((8, 2, 64), BF, gen).cuda() for _ in range(2))
+    pos = torch.arange(8, device="cuda")
+    calls = {"rope_fwd": lambda q, out: vx.rope_fwd(q, pos, cfg, out=out),
+             "append": lambda q, out: vx.paged_append(b.cache, 0, k, v, b.q_start, 5, rope=cfg, q=q, q_out=out),
+             "attn": lambda q, out: vx.paged_attn_fwd(b.cache, 0, q, b.q_start, 5, out=out)}
+    for name, call in calls.items():
+        want = call(row[:, 4:8].clone(), None)
+        for at in (0, 8):                              # before and behind the input's heads
+            x = row.clone()
+            got = call(x[:, 4:8], x[:, at:at + 4])
+            rest = [i for i in range(12) if not at <= i < at + 4]
+            assert torch.equal(got, want) and torch.equal(x[:, rest], row[:, rest]), name
+        x = torch.zeros(9, 12, 64, dtype=BF, device="cuda")
+        wrapped = torch.as_strided(x, (8, 4, 64), (768, 64, 1), 11 * 64)       # from a row's last head into the next row
+        for q, bad in ((x[:8, 4:8], x[:8, 5:9]), (x[:8, 4:8], x[:8, 1:5]), (x[:8, 4:8], x[:8, 7:11]),
+                       (x[:8, 4:8], x[1:, 4:8]), (x[:8, 0:4], wrapped), (wrapped, x[:8, 0:4])):
+            with pytest.raises(ValueError, match="overlaps"):
+                call(q, bad)
+
+
 # ----------------------------------------------------------------- refusals
 
 def test_a_kept_tensor_of_another_size_is_refused():

@@ -108,6 +108,18 @@ bool overlap(const Tensor& a, const Tensor& b) {
   const int64_t d = ((q - p) % row + row) % row;   // b's rows behind a's
   return d < extent(a, 1) || d + extent(b, 1) > row;
 }
+// Rows of a tensor that is written, which may not share elements with one another (an expanded tensor, say): rows of
+// heads, or heads of rows.
+vx_rows out_rows(const Tensor& t, const char* name, int64_t n, int64_t heads, int64_t dim, at::ScalarType dt, int dev) {
+  const vx_rows r = rows_of(t, name, n, heads, dim, dt, dev);
+  auto nested = [&](int64_t in, int64_t in_stride, int64_t over, int64_t over_stride) {
+    const int64_t row = in > 1 ? (in - 1) * in_stride + dim : dim;
+    return (in <= 1 || in_stride >= dim) && (over <= 1 || over_stride >= row);
+  };
+  if (t.numel() > 0 && !nested(t.size(1), r.head, n, r.row) && !nested(n, r.row, t.size(1), r.head))
+    value_error(std::string(name) + ": rows overlap one another");
+  return r;
+}
 bool same_rows(const Tensor& a, const Tensor& b) { return a.data_ptr() == b.data_ptr() && a.strides() == b.strides(); }
 
 cudaStream_t stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
@@ -215,7 +227,7 @@ Tensor rope_fwd(const Tensor& x, const Tensor& pos, int64_t rope, OptTensor out)
     out = new_rows(x);
   else if (!same_rows(*out, x) && overlap(x, *out))
     value_error("out overlaps x without being x");
-  const vx_rows yr = rows_of(*out, "out", n, heads, dim, x.scalar_type(), dev);
+  const vx_rows yr = out_rows(*out, "out", n, heads, dim, x.scalar_type(), dev);
   check(vx_rope_fwd(&xr, &yr, dt, n, static_cast<int>(std::min<int64_t>(heads, INT32_MAX)),
                     static_cast<int>(std::min<int64_t>(dim, INT32_MAX)), p, reinterpret_cast<const vx_rope_cfg*>(rope),
                     stream_of(dev)),
@@ -242,7 +254,7 @@ OptTensor paged_append(Cache& cache, int layer, const Tensor& k, const Tensor& v
       q_out = new_rows(*q);
     else if (!same_rows(*q_out, *q) && overlap(*q, *q_out))
       value_error("q_out overlaps q without being q");
-    qo = rows_of(*q_out, "q_out", n, q->size(1), c->head_dim, dt, cache.dev);
+    qo = out_rows(*q_out, "q_out", n, q->size(1), c->head_dim, dt, cache.dev);
   }
   Scratch s(ws, ws_bytes, kStatusBytes, cache.dev);
   check(vx_paged_append(c, layer, reinterpret_cast<const vx_rope_cfg*>(rope), q ? &qr : nullptr, q ? &qo : nullptr, heads,
@@ -281,7 +293,7 @@ py::object paged_attn_fwd(Cache& cache, int layer, const Tensor& q, const Tensor
     out = new_rows(q);
   else if (overlap(q, *out))
     value_error("out overlaps q");
-  const vx_rows orr = rows_of(*out, "out", n, heads, c->head_dim, dt, cache.dev);
+  const vx_rows orr = out_rows(*out, "out", n, heads, c->head_dim, dt, cache.dev);
   if (!lse && return_lse) lse = at::empty({n, heads}, q.options().dtype(at::kFloat));
   auto* lp = static_cast<float*>(whole(lse, "lse", at::kFloat, cache.dev, n * heads));
   const size_t need = ws != 0 ? 0 : vx_paged_attn_workspace(c, hq, n, max_q, max_kv, lp != nullptr, track.has_value());

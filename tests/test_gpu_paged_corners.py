@@ -202,3 +202,31 @@ def test_a_kept_tensor_of_another_size_is_refused():
     assert b.cache.lens.tolist() == before
     vx.paged_evict(b.cache, 0, 5, kept=kept(1, 2, 2, 0))
     assert b.cache.lens.tolist() == [0, 0]
+
+
+def test_outputs_whose_rows_overlap_are_refused():
+    vx = _vx()
+    b = Batch([30, 9], [5, 3], 4, 2, 64, 16, BF)
+    cfg, q = vx.RopeCfg(theta=1e4), b.q.cuda()
+    k, v = (torch.zeros(8, 2, 64, dtype=BF, device="cuda") for _ in range(2))
+    pos = torch.arange(8, device="cuda")
+    calls = [lambda q, out: vx.rope_fwd(q, pos, cfg, out=out),
+             lambda q, out: vx.paged_append(b.cache, 0, k, v, b.q_start, 5, rope=cfg, q=q, q_out=out),
+             lambda q, out: vx.paged_attn_fwd(b.cache, 0, q, b.q_start, 5, out=out)]
+    new = lambda *shape: torch.zeros(shape, dtype=BF, device="cuda")
+    for call in calls:
+        want = call(q, None)
+        for bad in (new(1, 4, 64).expand(8, 4, 64), new(8, 1, 64).expand(8, 4, 64), new(64).expand(8, 4, 64),
+                    torch.as_strided(new(4096), (8, 4, 64), (192, 64, 1)),
+                    torch.as_strided(new(4096), (8, 4, 64), (256, 32, 1))):
+            with pytest.raises(ValueError, match="overlap"):
+                call(q, bad)
+        heads_first = new(4, 8, 64).transpose(0, 1)
+        padded = new(8, 5, 3, 64)[:, 1:, 2]
+        for good in (heads_first, padded):
+            call(q, good)
+            assert torch.equal(good, want)
+    x = new(1, 4, 64).expand(8, 4, 64)                 # as an input it may be
+    vx.rope_fwd(x, pos, cfg)
+    with pytest.raises(ValueError, match="overlap"):
+        vx.rope_fwd(x, pos, cfg, out=x)

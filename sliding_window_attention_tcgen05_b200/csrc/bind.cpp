@@ -247,6 +247,7 @@ OptTensor paged_append(Cache& cache, int layer, const Tensor& k, const Tensor& v
   c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(cache.dev));
   vx_rows qr{}, qo{};
   int heads = 0;
+  if (q_out && !q) value_error("q_out without q");
   if (q) {
     qr = rows_of(*q, "q", n, -1, c->head_dim, dt, cache.dev);
     heads = static_cast<int>(std::min<int64_t>(q->size(1), INT32_MAX));

@@ -230,3 +230,11 @@ def test_outputs_whose_rows_overlap_are_refused():
     vx.rope_fwd(x, pos, cfg)
     with pytest.raises(ValueError, match="overlap"):
         vx.rope_fwd(x, pos, cfg, out=x)
+
+
+def test_an_output_for_no_queries_is_refused():
+    vx = _vx()
+    b = Batch([30], [5], 4, 2, 64, 16, BF)
+    k = torch.zeros(5, 2, 64, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="q_out"):
+        vx.paged_append(b.cache, 0, k, k, b.q_start, 5, rope=vx.RopeCfg(), q_out=torch.empty_like(b.q.cuda()))

@@ -112,6 +112,9 @@ class PagedCache:
         if name in self._TENSORS:
             object.__setattr__(self, "_described", None)   # described and checked again by the next call
 
+    def __getstate__(self):   # a copy or another process describes its own tensors
+        return {**self.__dict__, "_described": None}
+
     @property
     def device(self):
         return self.k.device

@@ -67,3 +67,20 @@ def test_it_is_rebuilt_for_another_torch(tmp_path, monkeypatch):
         except RuntimeError:
             pass
         assert len(runs) == n
+
+
+def test_a_cache_in_use_is_copied_and_pickled():
+    import copy
+    import pickle
+
+    import torch
+
+    import sliding_window_attention_tcgen05_b200 as vx
+    a = vx.PagedCache(1, 4, 16, 2, 64, 1, 4, weights=True, device="cpu")
+    a.table[0, 0] = 3
+    object.__setattr__(a, "_described", lambda: None)    # what a call leaves there cannot be pickled
+    for b in (copy.deepcopy(a), pickle.loads(pickle.dumps(a))):
+        assert b._described is None and a._described is not None
+        assert torch.equal(a.table, b.table) and a.table.data_ptr() != b.table.data_ptr()
+    b = copy.copy(a)
+    assert b._described is None and b.table is a.table

@@ -445,7 +445,8 @@ VX_API vx_status vx_paged_advance(const vx_paged_cache *cache, const int32_t *q_
  *   s = scale * q.k;  cap > 0: s = cap * tanh(s / cap);
  *   slopes (device fp32 [n_q_heads], NULL = none): s -= slopes[h] * |i - j|.
  * Distances count slots, so after an eviction they count the tokens kept.
- * scale <= 0 selects 1 / sqrt(head_dim). */
+ * scale <= 0 selects 1 / sqrt(head_dim), the largest is 1e18; cap is 0 (none)
+ * or 1e-18 .. 1e18. */
 typedef struct vx_attn_opts {
   float scale;
   float cap;

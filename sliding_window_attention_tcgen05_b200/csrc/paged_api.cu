@@ -386,8 +386,9 @@ vx_status vx_paged_attn_fwd(const vx_paged_cache* cache, int layer, const vx_row
   vx_attn_opts op = {};
   if (opts) op = *opts;
   VX_CHECK_ARG(op.window >= 0, "%s: window must be >= 0", what);
-  VX_CHECK_ARG(std::isfinite(op.cap) && op.cap >= 0.f && std::isfinite(op.scale),
-               "%s: cap must be finite and >= 0, scale finite", what);
+  // scale / cap and cap * 2 log2 e are formed in fp32.
+  VX_CHECK_ARG(op.cap == 0.f || (op.cap >= 1e-18f && op.cap <= 1e18f), "%s: cap must be 0 or 1e-18 .. 1e18", what);
+  VX_CHECK_ARG(std::isfinite(op.scale) && op.scale <= 1e18f, "%s: scale must be finite and at most 1e18", what);
   VX_CHECK_ARG((reinterpret_cast<uintptr_t>(op.prefix) & 3) == 0 && (reinterpret_cast<uintptr_t>(op.slopes) & 3) == 0 &&
                    (reinterpret_cast<uintptr_t>(lse) & 3) == 0,
                "%s: prefix, slopes or lse is misaligned", what);

@@ -392,7 +392,10 @@ typedef enum vx_rope_scaling {
   VX_ROPE_NTK = 2,     /* theta * factor^(rot_dim / (rot_dim - 2)) for theta     */
   VX_ROPE_YARN = 3     /* g f_m + (1 - g) f_m / factor with
                           g = clamp((orig_len f_m / 2 pi - beta_slow) / (beta_fast - beta_slow), 0, 1),
-                          cosine and sine times mscale                           */
+                          cosine and sine times mscale.  The ramp is linear in the turns
+                          orig_len f_m / 2 pi; where a checkpoint was trained with one
+                          that is linear in m between the pairs that make beta_fast and
+                          beta_slow turns, its frequencies between those two differ   */
 } vx_rope_scaling;
 
 /* Rotary positions: the first rot_dim elements of a head (even, <= head_dim;
@@ -400,8 +403,9 @@ typedef enum vx_rope_scaling {
  * when interleaved, by position * f_m, f_m = theta^(-2m / rot_dim); the others
  * are copied.  scaling != VX_ROPE_NONE needs factor >= 1.  VX_ROPE_YARN needs
  * orig_len >= 1 and beta_fast > beta_slow; mscale 0 selects
- * 0.1 ln(factor) + 1.  The angle is kept as a 64-bit fraction of a turn, so
- * positions of any size are exact to better than 2^-24 of a radian. */
+ * 0.1 ln(factor) + 1.  The angle is kept as a 64-bit fraction of a turn; it is
+ * off by at most pi 2^-25 (one rounding to fp32) and |pos| 2^-61 turns (of the
+ * frequencies), together below 2^-22 of a radian for |pos| < 2^35. */
 typedef struct vx_rope_cfg {
   int rot_dim;
   int interleaved;
@@ -416,7 +420,7 @@ typedef struct vx_rope_cfg {
 /* y = rotary(x) at positions pos[t] (device int64 [n_tokens], any sign), for
  * n_heads heads of head_dim (2 .. 256, even) elements; dt VX_F32 or VX_BF16,
  * arithmetic in fp32.  y may be x itself (the same rows), but must not
- * overlap it otherwise. */
+ * overlap it otherwise; the rows of y must not overlap one another. */
 VX_API vx_status vx_rope_fwd(const vx_rows *x, const vx_rows *y, vx_dtype dt, int64_t n_tokens, int n_heads,
                              int head_dim, const int64_t *pos, const vx_rope_cfg *rope, cudaStream_t stream);
 
@@ -424,8 +428,9 @@ VX_API vx_status vx_rope_fwd(const vx_rows *x, const vx_rows *y, vx_dtype dt, in
  * cache's dtype) to slots lens[s] + t of layer `layer`, zeroes acc there, and
  * leaves lens and pos alone.  With rope (may be NULL), k is rotated at
  * positions pos[s] + t on its way, and so is q (may be NULL; n_q_heads heads)
- * into q_out (which may be q itself); without rope q must be NULL.  Rows must
- * start on 16-byte boundaries.  Two sequences of one call must not append to
+ * into q_out (which may be q itself, but must not overlap q otherwise, nor k or
+ * v, nor may its rows overlap one another); without rope q must be NULL.  Rows
+ * must start on 16-byte boundaries.  Two sequences of one call must not append to
  * the same page.  Workspace: 256 bytes (the status word). */
 VX_API vx_status vx_paged_append(const vx_paged_cache *cache, int layer, const vx_rope_cfg *rope, const vx_rows *q,
                                  const vx_rows *q_out, int n_q_heads, const vx_rows *k, const vx_rows *v,
@@ -459,18 +464,25 @@ typedef struct vx_attn_opts {
  * them (vx_paged_append): per query head h, o = softmax(s) v over the K/V head
  * h / (n_q_heads / n_kv_heads), and lse (fp32 [n_tokens, n_q_heads], may be
  * NULL) = log of the sum of exp(s).  A query that sees nothing gets zeros and
- * lse -inf.  VX_BF16: tensor cores, fp32 softmax and sums; VX_F32: fp32
- * throughout.
- * q, o: rows of n_q_heads heads, dtype of the cache.  max_kv bounds lens[s] + n
+ * lse -inf.  VX_BF16: tensor cores; scores, softmax statistics, weights' sums
+ * and outputs are accumulated in fp32 with the hardware's exponential (a few
+ * 2^-23), and each weight is rounded to bf16 for its product with v, as the
+ * tensor cores take it (lse and the accumulated weights are of the unrounded
+ * ones).  VX_F32: fp32 throughout.
+ * q, o: rows of n_q_heads heads, dtype of the cache; o must not overlap q or
+ * the cache, nor its rows one another.  max_kv bounds lens[s] + n
  * over the sequences (0 = max_pages * page_size; only the split of the work
  * depends on it).  opts may be NULL (all zero).
  * track != 0 adds up, per K/V head and slot j < lens[s] + n, the softmax
  * weights that slot j got from the chunk's queries and the group's heads:
  *   acc_j = track_decay * acc_j + sum      (track_decay 0 does not read acc).
+ * Sequences without rows in the chunk keep their acc as it is.
  * The sums' order is fixed, so equal calls give equal bits.
  * K and V rows of slots that no query of the chunk sees may hold anything,
- * infinities and NaN too; a non-finite V row that some query sees can reach
- * the other queries of the same 256-row tile.
+ * infinities and NaN too.  A non-finite K row reaches only the queries that see
+ * it, a non-finite query only the weights of the slots that it sees; a
+ * non-finite V row that some query sees can reach the other queries of the same
+ * 256-row tile.
  * Workspace: vx_paged_attn_workspace(). */
 VX_API vx_status vx_paged_attn_fwd(const vx_paged_cache *cache, int layer, const vx_rows *q, const vx_rows *o,
                                    float *lse, int n_q_heads, const int32_t *q_start, int64_t n_tokens, int max_q,

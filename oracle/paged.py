@@ -52,7 +52,7 @@ def seen(old, n, window=0, prefix=0):
 def attention(q, k, v, old, window=0, prefix=0, cap=0.0, slopes=None, scale=0.0):
     """q [n, Hq, D], k, v [old + n, Hkv, D] -> dict of o [n, Hq, D], lse [n, Hq], weights [Hkv, old + n] (summed over
     queries and the group), absv = softmax-weighted |v| [n, Hq, D], smax = the largest sum |q k| * scale of a row's
-    visible keys [n, Hq], absw = sum over queries of p * (1 + smax) [Hkv, old + n].  Masked k and v are not read."""
+    visible keys [n, Hq].  Masked k and v are not read."""
     n, Hq, D = q.shape
     L, Hkv, _ = k.shape
     G = Hq // Hkv
@@ -65,7 +65,7 @@ def attention(q, k, v, old, window=0, prefix=0, cap=0.0, slopes=None, scale=0.0)
     dist = np.abs(old + np.arange(n)[:, None] - np.arange(L)[None, :])
     o, absv = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
     lse, smax = np.full((n, Hq), -np.inf), np.zeros((n, Hq))
-    w, absw = np.zeros((Hkv, L)), np.zeros((Hkv, L))
+    w = np.zeros((Hkv, L))
     some = m.any(1)
     for h in range(Hq):
         kh = h // G
@@ -86,8 +86,7 @@ def attention(q, k, v, old, window=0, prefix=0, cap=0.0, slopes=None, scale=0.0)
             lse[:, h] = np.where(some, top + np.log(z), -np.inf)
         smax[:, h] = big.max(1, initial=0.0)
         w[kh] += p.sum(0)
-        absw[kh] += (p * (1.0 + smax[:, h])[:, None]).sum(0)
-    return dict(o=o, lse=lse, weights=w, absv=absv, smax=smax, absw=absw)
+    return dict(o=o, lse=lse, weights=w, absv=absv, smax=smax)
 
 
 def evict(acc, keep, recent):

@@ -106,7 +106,7 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
 // multiplication by scale * log2(e).  A cap in bf16: where all of a thread's
 // scores are at most half the cap, as they are nearly always, cap * tanh(z) =
 // score * P(z^2) with the minimax polynomial P of tanh(z) / z on z^2 <= 1/4
-// (relative error 1.3e-8), on the FMA pipe alone; else cap * (1 - 2 / (e^{2z} +
+// (relative error 2.8e-8), on the FMA pipe alone; else cap * (1 - 2 / (e^{2z} +
 // 1)), from one exponential and half a reciprocal (absolute error about cap *
 // 2^-22, where the hardware's own tanh would leave cap * 2^-11).  fp32: tanhf,
 // whose error is relative to the score too.

@@ -19,7 +19,9 @@ namespace {
 // of every row looked up one tile ahead; O is rescaled only when a row's
 // maximum grows by more than 2^8; the four warps' softmax states, and those of
 // up to 8 CTAs of a sequence (a cluster), are joined through shared memory at
-// the end.
+// the end.  Weights are rounded to bf16 for the product with V (mma.sync takes
+// both operands as bf16), as in the tcgen05 kernel; their sum is of the
+// unrounded ones.
 constexpr int kRowsThreads = 128;
 constexpr int kRowsStages = 2;
 constexpr int kRowsStageBytes = 8192;   // K and V of one warp tile

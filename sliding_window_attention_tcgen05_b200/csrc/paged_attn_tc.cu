@@ -19,7 +19,12 @@ namespace {
 // layout (zeros for the others).  K and V tiles alternate in one ring.
 // A warp per warpgroup issues O += P V as P arrives (written over S as bf16, 64
 // keys at a time), then the next S = Q K^T.  O is rescaled in place only when
-// a row's maximum grows by more than 2^8.
+// a row's maximum grows by more than 2^8.  P is the one thing held in fewer
+// bits than fp32: kind::f16 products take both operands as bf16 where V is
+// bf16.  That rounding, 2^-9 of a weight at random, is as large as the output's
+// own (against float64, relative: 2.0e-3 to 2.4e-3, of which the output's
+// rounding alone makes 1.65e-3); P as two bf16 terms would double the products
+// with V.  l sums the unrounded weights, so that lse has no part in it.
 //
 // What bounds it: a warpgroup's chain of softmax (about 1700 cycles a tile,
 // 1024 of them MUFU issue), products (12 x 64 behind the last weights) and

@@ -75,8 +75,10 @@ __device__ __forceinline__ int slot_row(const PagedView& c, int s, int head, int
 
 // ---------------------------------------------------------------- rotary --
 // Angles as fractions of a turn: turns[m] = round(f_m / 2 pi * 2^64), so
-// pos * turns[m] mod 2^64 is the fraction of a turn of pos * f_m exactly up to
-// |pos| * 2^-65 turns, for any 64-bit position.
+// pos * turns[m] mod 2^64 is the fraction of a turn of pos * f_m up to |pos|
+// times the error of turns[m]: 2^-65 of its rounding and, f_m being a product of
+// up to seven powers in 64-bit mantissas, a few 2^-64 of f_m's own, together
+// below 2^-61.
 constexpr int kMaxRotPairs = 128;
 constexpr int kMaxTok = 32;   // tokens of a block
 struct RopeTable {
@@ -164,7 +166,6 @@ struct PagedAttnPlan {
 };
 PagedAttnPlan plan_paged_attn(bool bf16, int head_dim, int n_seqs, int n_kv_heads, int group, int max_q,
                               int64_t max_kv);
-cudaError_t launch_paged_attn(const Launch& L, const PagedAttnArgs& a, const PagedAttnPlan& plan, bool bf16);
 
 // -------------------------------------------------------------- eviction --
 struct EvictArgs {

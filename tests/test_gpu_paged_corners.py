@@ -90,6 +90,78 @@ def test_fp32_weights_below_the_smallest_normal_number_are_not_flushed(n, hq, kv
     assert not got[old:].any()
 
 
+# -------------------------------------------------------------- far angles
+
+def _exact_angles(pos, rot, theta, scaling, factor, orig_len):
+    """pos * f_m mod 2 pi in 60 digits, and the factor on cosine and sine; beta 32 and 1."""
+    from decimal import Decimal as Dec, getcontext
+    getcontext().prec = 60
+    pi = Dec("3.14159265358979323846264338327950288419716939937510582097494459")
+    theta, factor, ms = Dec(theta), Dec(factor), 1.0
+    if scaling == "ntk":
+        theta *= (factor.ln() * rot / (rot - 2)).exp()
+    out = []
+    for m in range(rot // 2):
+        f = (theta.ln() * (-2 * m) / rot).exp()
+        if scaling == "linear":
+            f /= factor
+        if scaling == "yarn":
+            g = min(max((orig_len * f / (2 * pi) - 1) / 31, Dec(0)), Dec(1))
+            f = g * f + (1 - g) * f / factor
+            ms = 0.1 * np.log(float(factor)) + 1.0
+        out.append([float(Dec(int(p)) * f % (2 * pi)) for p in pos])
+    return np.array(out).T, ms
+
+
+@pytest.mark.parametrize("rot,theta,scaling,factor,orig_len", [
+    (64, 1e6, "none", 1.0, 0), (128, 1e4, "none", 1.0, 0), (64, 1.0, "none", 1.0, 0), (128, 5e5, "linear", 3.0, 0),
+    (64, 1e6, "ntk", 4.0, 0), (128, 1e6, "yarn", 4.0, 32768), (34, 1e4, "yarn", 8.0, 2048)])
+def test_rotary_angles_of_far_positions(rot, theta, scaling, factor, orig_len):
+    # The bound that vx.h states: pi 2^-25 and |pos| 2^-61 turns; sine and cosine of an angle off by e are off by e.
+    vx = _vx()
+    pos = np.array([0, 1, -1, 12345, 2 ** 20 + 3, -(2 ** 31) - 5, 2 ** 35 - 1, 2 ** 40 + 12345, -(2 ** 45) + 7, 2 ** 50 + 1])
+    x = torch.zeros(len(pos), 1, rot, device="cuda")
+    x[..., :rot // 2] = 1.0                                  # y = (cos, sin), each rounded twice, sincos 2 U
+    cfg = vx.RopeCfg(theta=theta, scaling=scaling, factor=factor, orig_len=orig_len)
+    got = _host(vx.rope_fwd(x, torch.from_numpy(pos).cuda(), cfg))[:, 0]
+    ang, ms = _exact_angles(pos, rot, theta, scaling, factor, orig_len)
+    tol = ms * (np.pi * 2.0 ** -25 + np.abs(pos.astype(np.float64))[:, None] * 2.0 ** -61 * 2 * np.pi + 4 * U)
+    _within(got[:, :rot // 2], ms * np.cos(ang), tol, "cosines")
+    _within(got[:, rot // 2:], ms * np.sin(ang), tol, "sines")
+
+
+def test_rotary_angles_wrap_exactly():
+    # theta 1: all frequencies are 1, one turn's fraction is known to the bit and wraps in 64 bits at any position.
+    vx = _vx()
+    from decimal import Decimal as Dec, getcontext
+    getcontext().prec = 60
+    pi = Dec("3.14159265358979323846264338327950288419716939937510582097494459")
+    turns = int(Dec(2) ** 64 / (2 * pi) + Dec("0.5"))
+    pos = [2 ** 62 + 1, -(2 ** 63), 2 ** 63 - 1, -(2 ** 55) - 3]
+    x = torch.zeros(len(pos), 1, 64, device="cuda")
+    x[..., :32] = 1.0
+    got = _host(vx.rope_fwd(x, torch.tensor(pos).cuda(), vx.RopeCfg(theta=1.0)))[:, 0]
+    for r, p in enumerate(pos):
+        # f = 1 is exact; 2 pi and the quotient are rounded to 64-bit mantissas: turns may be off by one
+        angs = [float(Dec(p * (turns + e) % 2 ** 64) / 2 ** 63 * pi) for e in (-1, 0, 1)]
+        tol = np.pi * 2.0 ** -25 + 4 * U
+        assert any(np.all(np.abs(got[r, :32] - np.cos(a)) <= tol) and np.all(np.abs(got[r, 32:] - np.sin(a)) <= tol)
+                   for a in angs)
+
+
+# ---------------------------------------------- sequences without new tokens
+
+@pytest.mark.parametrize("dtype,n", [(BF, 1), (BF, 12), (BF, 150), (F32, 1), (F32, 70)])
+@pytest.mark.parametrize("track", [0.0, 0.5])
+def test_weights_of_sequences_without_rows_stay(dtype, n, track):
+    vx = _vx()
+    b = Batch([90, 50, 7], [0, n, 0], 4, 2, 64, 16, dtype, weights=True)
+    vx.paged_attn_fwd(b.cache, 0, b.q.cuda(), b.q_start, n, track=track)
+    for s in (0, 2):
+        assert torch.equal(b.gather(b.cache.acc, s, b.olds[s])[0], b.acc[s][0].T)
+    assert not torch.equal(b.gather(b.cache.acc, 1, 50)[0], b.acc[1][0].T[:50])
+
+
 # ------------------------------------------------------- status and scratch
 
 def test_a_full_table_is_still_reported_after_the_workspace_has_grown():
@@ -238,3 +310,38 @@ def test_an_output_for_no_queries_is_refused():
     k = torch.zeros(5, 2, 64, dtype=BF, device="cuda")
     with pytest.raises(ValueError, match="q_out"):
         vx.paged_append(b.cache, 0, k, k, b.q_start, 5, rope=vx.RopeCfg(), q_out=torch.empty_like(b.q.cuda()))
+
+
+# ----------------------------------------------------------------- eviction
+
+@pytest.mark.parametrize("cap,lens,lanes", [(50000, 50000, 160), (50000, 700, 160), (9000, 9000, 160), (400000, 400000, 2)])
+@pytest.mark.parametrize("kind", ["rand", "ties", "equal"])
+def test_eviction_by_the_tables_capacity(cap, lens, lanes, kind):
+    # Keys that fit in shared memory and keys that do not, by one CTA for each of many heads and by clusters for a few.
+    vx = _vx()
+    page, D, keep, recent = 500, 64, lens // 3, lens // 50
+    pages = cap // page
+    c = vx.PagedCache(1, pages, page, lanes, D, 1, pages, weights=True)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    c.table.copy_(torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)[None])
+    a = torch.rand(lanes, lens, generator=gen, device="cuda")
+    if kind == "ties":
+        a = torch.randint(0, 5, (lanes, lens), generator=gen, device="cuda").float()
+    if kind == "equal":
+        a.fill_(0.25)
+    j = torch.arange(lens, device="cuda")
+    pg, off = c.table[0].long()[j // page], j % page
+    c.acc[0][pg, :, off] = a.T
+    c.k[0][pg, :, off] = (j % 251).to(BF)[:, None, None].expand(lens, lanes, D)
+    c.v[0][pg, :, off] = (j % 241).to(BF)[:, None, None].expand(lens, lanes, D)
+    c.lens.fill_(lens)
+    kept = torch.full((1, 1, lanes, keep), -1, dtype=torch.int32, device="cuda")
+    vx.paged_evict(c, keep, recent, kept=kept)
+    best = torch.sort(a[:, :lens - recent], dim=1, descending=True, stable=True).indices[:, :keep - recent].sort(1).values
+    want = torch.cat([best, torch.arange(lens - recent, lens, device="cuda").expand(lanes, recent)], 1)
+    assert torch.equal(kept[0, 0].long(), want)
+    i = torch.arange(keep, device="cuda")
+    pg, off = c.table[0].long()[i // page], i % page
+    assert torch.equal(c.acc[0][pg, :, off].T, a.gather(1, want))
+    assert torch.equal(c.k[0][pg, :, off][..., 5].T, (want % 251).to(BF))
+    assert torch.equal(c.v[0][pg, :, off][..., 60].T, (want % 241).to(BF))

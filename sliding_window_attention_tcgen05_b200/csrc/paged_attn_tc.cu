@@ -259,7 +259,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         const uint32_t empty = (((2 * u + (is_v ? 1 : 0)) / NST) & 1) ^ 1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) row[k] = next[k];
-        const int used = tc_rows(it, u);   // rows that the product with V reads
+        // Rows that the product with V reads; of K all, where a cap's formula is chosen by a row's largest score (what lay
+        // behind the list's end before may not choose it).
+        const int used = MOD && !is_v && a.cap > 0.f ? kTcKeys : tc_rows(it, u);
         // No free buffer: nothing to issue, so pass on what lands meanwhile.
         if (!tma)
           while (told < u && !__all_sync(0xffffffffu, mbar_test_wait(bar(EMPTY + st), empty))) landed(u - told - 1);

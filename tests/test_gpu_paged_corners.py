@@ -67,6 +67,25 @@ def test_a_query_that_is_not_finite_leaves_the_weights_of_slots_it_does_not_see(
     _within(got, want, 1.01 * r["weights"] * rel + 4 * U * r["weights"] + 1e-30, "weights")
 
 
+# ------------------------------------------------------------------ same bits
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (64, 50), (128, 50)])
+def test_what_earlier_calls_left_in_shared_memory_changes_no_bit(D, page):
+    # Capped scores over lists that end inside a tile, behind calls whose keys are large, tiny or not finite.
+    vx = _vx()
+    b = Batch([30] * 60, [40] * 60, 4, 2, D, page, BF, weights=True, scale=1.5)
+    q, res = b.q.cuda(), []
+    full = Batch([88] * 60, [40] * 60, 4, 2, D, page, BF)
+    for x in (0.0, 1e30, 3.0, float("nan"), -1e30, float("inf")):
+        full.cache.k.fill_(x)
+        vx.paged_attn_fwd(full.cache, 0, full.q.cuda(), full.q_start, 40)
+        o, lse = vx.paged_attn_fwd(b.cache, 0, q, b.q_start, 40, cap=12.0, track=0.0, return_lse=True)
+        res.append((o, lse, b.cache.acc.clone()))
+    _check_attn(b, *res[0][:2], cap=12.0)
+    for r in res[1:]:
+        assert all(torch.equal(x.nan_to_num(), y.nan_to_num()) for x, y in zip(r, res[0]))
+
+
 # ------------------------------------------------------------ fp32 throughout
 
 @pytest.mark.parametrize("n,hq,kv", [(1, 2, 0), (1, 2, 16), (4, 4, 0), (12, 2, 0), (70, 4, 0)])

@@ -66,7 +66,7 @@ __device__ __forceinline__ void st1(void* p, int64_t e, float x) {
 // 2 pairs / V units of one vector; then (D - 2 pairs) / V copies.
 //
 // A thread takes one unit at a time: what counts is the number of threads in
-// flight (16384 rows of 40 heads of 128, bf16: 57 us, 89% of copy bandwidth; two
+// flight (16384 rows of 40 heads of 128, bf16: 59 us, 87% of copy bandwidth; two
 // units a thread at 48 registers 66, four at 78 registers 77).
 constexpr int kRopeBlocks = 6;   // resident blocks an SM: at most 40 registers
 constexpr int kAppendBlocks = 5;   // 48 (prompts of up to 4001 tokens, 32 + 8 + 8 heads of 128: 68 us; at 64 registers 72)

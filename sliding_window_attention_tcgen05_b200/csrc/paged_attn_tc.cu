@@ -32,8 +32,9 @@ namespace {
 // So what counts is that one warpgroup's chain runs under the other's: the
 // warps that share a scheduler take turns at their exponentials (left alone the
 // warpgroups fall into step).  Measured for 4 ragged prompts of up to 4096
-// tokens over 8192, 32/8 heads of 128 (819 GFLOP): 780 us (1050 TFLOP/s, 64% of
-// cuBLAS's burst rate); without the turns 837; all weights handed over at once
+// tokens over 8192, 32/8 heads of 128 (819 GFLOP), 20 passes at 1965 MHz: 780 us
+// (1050 TFLOP/s, 64% of cuBLAS's burst rate; back to back under the power cap,
+// at 1.72 GHz, 875); without the turns 837; all weights handed over at once
 // 828, in three parts 830; a quarter of the exponentials on the FMA pipe
 // (range reduction and a polynomial) 895; rows all by cp.async, which feeds an
 // SM 16 bytes a clock, 1026; TMA gathers of four rows 1276.

@@ -249,6 +249,70 @@ def test_tensors_resized_in_place_are_described_again():
             vx.paged_advance(c, torch.zeros(4, dtype=torch.int32, device="cuda"), 0, 0)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,D,page", [(2, 64, 16), (12, 128, 16), (150, 64, 16), (150, 128, 64), (150, 128, 7), (70, 64, 256)])
+def test_pages_outside_the_pool_read_as_zeros_and_are_reported(dtype, n, D, page):
+    vx = _vx()
+    b = Batch([300, 45], [n, n], 4, 2, D, page, dtype, weights=True)
+    c, pages = b.cache, b.cache.k.shape[1]
+    ws = vx.Workspace(1 << 24)
+    first = min(64 // page, b.olds[0] // page - 1)
+    for bad in (-1, pages, 2 ** 31 - 1, -2 ** 31):
+        good = c.table[0, first].clone()
+        c.table[0, first] = bad
+        rows = slice(first * page, (first + 1) * page)
+        k, v = b.k[0][:, rows].clone(), b.v[0][:, rows].clone()
+        b.k[0][:, rows], b.v[0][:, rows] = 0, 0
+        vx.status_reset(ws)
+        o, lse = vx.paged_attn_fwd(c, 0, b.q.cuda(), b.q_start, n, return_lse=True, ws=ws)
+        assert vx.status_check(ws) == 1 and "sequence 0" in vx.lib.vx_last_error().decode()
+        _check_attn(b, o, lse)
+        c.table[0, first] = good
+        b.k[0][:, rows], b.v[0][:, rows] = k, v
+    acc = c.acc.clone()
+    c.table[0, first] = -1                                   # the weights of the other slots, none written for the page
+    vx.status_reset(ws)
+    vx.paged_attn_fwd(c, 0, b.q.cuda(), b.q_start, n, track=0.0, ws=ws)
+    assert vx.status_check(ws) == 1
+    lost = int(b.table[0][first])
+    assert torch.equal(c.acc[:, lost].nan_to_num(), acc[:, lost].nan_to_num())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [2, 12, 150])
+def test_lengths_outside_the_table_are_clamped_and_reported(dtype, n):
+    vx = _vx()
+    b = Batch([100, 45], [n, n], 4, 2, 64, 16, dtype, weights=True)
+    c, q, ws = b.cache, b.q.cuda(), vx.Workspace(1 << 24)
+    gen = torch.Generator().manual_seed(6)
+    k, v = (_randn((b.n, 2, 64), dtype, gen).cuda() for _ in range(2))
+    cap = c.table.shape[1] * 16
+    vx.paged_append(c, 0, k, v, b.q_start, n)
+    want = vx.paged_attn_fwd(c, 0, q, b.q_start, n, track=0.0, return_lse=True)
+    acc = b.gather(c.acc, 1, 45 + n)
+    for bad in (-1, -2 ** 63, cap + 1, 2 ** 40, 2 ** 63 - 1):
+        c.lens.copy_(torch.tensor([bad, 45]))
+        calls = [lambda: vx.paged_append(c, 0, k, v, b.q_start, n, ws=ws),
+                 lambda: vx.paged_attn_fwd(c, 0, q, b.q_start, n, track=0.0, return_lse=True, ws=ws),
+                 lambda: vx.paged_advance(c, b.q_start, b.n, n, ws=ws)]
+        for i, call in enumerate(calls):
+            vx.status_reset(ws)
+            got = call()
+            assert vx.status_check(ws) == 1 and "sequence 0" in vx.lib.vx_last_error().decode()
+            if i == 1:                                       # the other sequence does not notice
+                for x, y in zip(got, want):
+                    assert torch.equal(x[n:], y[n:])
+                assert torch.equal(b.gather(c.acc, 1, 45 + n), acc)
+        assert c.lens.tolist() == [min(n, cap) if bad < 0 else cap, 45 + n]
+        c.lens.copy_(torch.tensor([bad, 45]))
+        dst = vx.PagedCache(1, c.k.shape[1], 16, 2, 64, 2, c.table.shape[1], dtype=dtype, weights=True)
+        dst.table.copy_(torch.arange(dst.table.numel()).reshape(dst.table.shape) % c.k.shape[1])
+        dst.table[1] = torch.arange(dst.table.shape[1]) + c.k.shape[1] - dst.table.shape[1]
+        vx.status_reset(ws)
+        vx.paged_evict(c, 10, 4, dst=dst, ws=ws)
+        assert vx.status_check(ws) == 1 and dst.lens.tolist() == [0 if bad < 0 else 10, 10]
+
+
 # -------------------------------------------------- tensors in one fused row
 
 def test_outputs_may_be_other_heads_of_the_inputs_rows():
